@@ -335,6 +335,91 @@ mq_status mq_attention_decode_bf16(const void *qkv_bf16, int64_t m, int64_t pos0
                                    int64_t S_max, void *o_bf16, void *workspace, size_t ws_bytes,
                                    cudaStream_t stream);
 
+/* ---- serving: many sequences at once over a paged KV cache --------------------
+ * Mix-Quant's prefill workers build the KV cache that decode workers read
+ * (gist.science technical summary, section 2 "System-Level Deployment"); the
+ * pages do not say how it is kept.  Here it is two device BF16 arrays
+ * [n_pages, Hkv, page_size, 128] (keys, values).  A sequence's cache is the
+ * pages its row of block_table (device int32 [B, max_pages]) names: position
+ * p lies in page block_table[b][p / page_size], and slot s (int64) means row
+ * s % page_size of page s / page_size.  page_size is a power of two from 8 to
+ * 256.  A step's new tokens are packed: those of sequence b are rows
+ * cu[b] .. cu[b + 1] - 1 of the batch (device int32 [B + 1], ascending, from
+ * 0; a sequence may have none), and rows from cu[B] on (padding up to T) are
+ * neither read nor written.  All lengths, tables and slots are read on the
+ * device, so a captured graph can be replayed with new ones; only T, B and
+ * max_new are fixed by the call. */
+
+/* Limits of B and T of the calls below. */
+#define MQ_PAGED_MAX_REQUESTS 16384
+#define MQ_PAGED_MAX_TOKENS (1 << 22)
+
+/* The page plan of a step: sequence b holds ctx_lens[b] cached tokens (its
+ * first ceil(ctx / page_size) table entries are in place) and gets
+ * new_lens[b] more (device int32 [B] both; negative counts as 0).  Pages are
+ * taken from free_pages (device int32 [n_free]) in the order of the
+ * sequences.  Writes, on the device:
+ *   cu_new [B + 1]: first row of each sequence, cut at T;
+ *   block_table (device int32 [B, max_pages]): the entries of the new pages,
+ *     all others left as they are;
+ *   slots [T] (int64): the cache slot of each row; -1 for rows past cu_new[B]
+ *     and for tokens that got no page (free_pages or the table row is used
+ *     up, or the table names a negative page);
+ *   info [4] (int32): new tokens asked for, pages needed (the first info[1]
+ *     of free_pages are now in use), tokens of the first count without a slot
+ *     (cut at T, or without a page), and the longest ctx + new.
+ * Errors: MQ_ERR_INVALID_ARG (null pointer), MQ_ERR_SHAPE (B, T, page_size,
+ * max_pages out of range), MQ_ERR_ALIGNMENT (natural alignment). */
+mq_status mq_paged_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
+                        const int32_t *free_pages, int64_t n_free, int32_t *block_table,
+                        int64_t max_pages, int64_t T, int32_t *cu_new, int64_t *slots, int32_t *info,
+                        cudaStream_t stream);
+
+/* Scratch bytes of mq_attention_packed_bf16 (0 for invalid sizes). */
+size_t mq_attention_packed_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hkv, int64_t D);
+
+/* Causal attention of B packed prompts (arithmetic, head layout and limits of
+ * mq_attention_prefill_bf16; each row attends over the rows of its own prompt
+ * up to itself): qkv (device BF16, T rows of (H + 2 Hkv) * 128, leading
+ * dimension ldqkv, a multiple of 8) -> o (device BF16, T rows of H * 128,
+ * leading dimension ldo, a multiple of 8).  With slots (device int64 [T]; NULL
+ * skips the cache, then k_pages and v_pages are NULL too) each row's keys and
+ * values are also written to its slot; rows whose slot is outside the cache
+ * are not.  No two rows may name one slot.  o_amax (device, one float, or
+ * NULL) receives max |o| over the rows below cu_lens[B], ready for
+ * mq_quantize_nvfp4 with n_partials = 1.  A non-finite key or value reaches
+ * only rows that attend to it.  Requirements: D == 128, H % Hkv == 0,
+ * H / Hkv <= 128, H <= 1024; qkv, o, pages and workspace 16-byte aligned;
+ * workspace (device) of at least mq_attention_packed_workspace_bytes bytes,
+ * not shared with a call that may run at the same time.  Bounded waits: a
+ * timeout is latched and reported by mq_check. */
+mq_status mq_attention_packed_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t T, const int32_t *cu_lens,
+                                   int64_t B, int64_t H, int64_t Hkv, int64_t D, const int64_t *slots,
+                                   void *k_pages, void *v_pages, int64_t n_pages, int64_t page_size,
+                                   void *o_bf16, int64_t ldo, float *o_amax, void *workspace,
+                                   size_t ws_bytes, cudaStream_t stream);
+
+/* Scratch bytes of mq_attention_paged_bf16 (0 for invalid sizes). */
+size_t mq_attention_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
+                                          int64_t D);
+
+/* Attention of new tokens over the paged cache: chunks of a prompt, draft
+ * tokens, single decode tokens, or a mix of them.  The rows' keys and values
+ * are first written to their slots (slots NULL: they are in the cache
+ * already); row t of sequence b, at position pos = ctx_lens[b] + t -
+ * cu_new[b], then attends over cache positions 0 .. pos through
+ * block_table[b] (positions past max_pages * page_size are dropped; a page
+ * outside the cache reads as zeros).  qkv, o, o_amax, slots, requirements and
+ * workspace as in mq_attention_packed_bf16; max_new (1 .. T) bounds the new
+ * tokens of every sequence (rows beyond it are not computed) and lets the call
+ * choose its launch, so pass 1 for a plain decode step. */
+mq_status mq_attention_paged_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t T, const int32_t *cu_new,
+                                  const int32_t *ctx_lens, int64_t B, int64_t max_new, int64_t H,
+                                  int64_t Hkv, int64_t D, const int64_t *slots, const int32_t *block_table,
+                                  int64_t max_pages, void *k_pages, void *v_pages, int64_t n_pages,
+                                  int64_t page_size, void *o_bf16, int64_t ldo, float *o_amax,
+                                  void *workspace, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

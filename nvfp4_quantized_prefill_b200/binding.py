@@ -48,6 +48,13 @@ SIGNATURES = [
     ("mq_attention_decode_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64]),
     ("mq_attention_decode_bf16", _I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _SZ,
                                       _P]),
+    ("mq_paged_plan", _I, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P]),
+    ("mq_attention_packed_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64]),
+    ("mq_attention_packed_bf16", _I, [_P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64,
+                                      _P, _P, _SZ, _P]),
+    ("mq_attention_paged_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    ("mq_attention_paged_bf16", _I, [_P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _P,
+                                     _I64, _I64, _P, _I64, _P, _P, _SZ, _P]),
 ]
 
 _lib = None
@@ -260,4 +267,36 @@ def mq_attention_decode_bf16(qkv, m: int, pos0: int, H: int, Hkv: int, D: int, k
                              S_max: int, o, workspace, ws_bytes: int, stream=None) -> None:
     _ok("mq_attention_decode_bf16", lib().mq_attention_decode_bf16(
         _ptr(qkv), m, pos0, H, Hkv, D, _ptr(k_cache), _ptr(v_cache), S_max, _ptr(o), _ptr(workspace),
+        ws_bytes, _stream(stream)))
+
+
+def mq_paged_plan(ctx_lens, new_lens, B: int, page_size: int, free_pages, n_free: int, block_table, max_pages: int,
+                  T: int, cu_new, slots, info, stream=None) -> None:
+    _ok("mq_paged_plan", lib().mq_paged_plan(
+        _ptr(ctx_lens), _ptr(new_lens), B, page_size, _ptr(free_pages), n_free, _ptr(block_table), max_pages, T,
+        _ptr(cu_new), _ptr(slots), _ptr(info), _stream(stream)))
+
+
+def mq_attention_packed_workspace_bytes(T: int, B: int, H: int, Hkv: int, D: int) -> int:
+    return int(lib().mq_attention_packed_workspace_bytes(T, B, H, Hkv, D))
+
+
+def mq_attention_packed_bf16(qkv, ldqkv: int, T: int, cu_lens, B: int, H: int, Hkv: int, D: int, slots, k_pages,
+                             v_pages, n_pages: int, page_size: int, o, ldo: int, o_amax, workspace, ws_bytes: int,
+                             stream=None) -> None:
+    _ok("mq_attention_packed_bf16", lib().mq_attention_packed_bf16(
+        _ptr(qkv), ldqkv, T, _ptr(cu_lens), B, H, Hkv, D, _ptr(slots), _ptr(k_pages), _ptr(v_pages), n_pages,
+        page_size, _ptr(o), ldo, _ptr(o_amax), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def mq_attention_paged_workspace_bytes(T: int, B: int, max_new: int, H: int, Hkv: int, D: int) -> int:
+    return int(lib().mq_attention_paged_workspace_bytes(T, B, max_new, H, Hkv, D))
+
+
+def mq_attention_paged_bf16(qkv, ldqkv: int, T: int, cu_new, ctx_lens, B: int, max_new: int, H: int, Hkv: int, D: int,
+                            slots, block_table, max_pages: int, k_pages, v_pages, n_pages: int, page_size: int, o,
+                            ldo: int, o_amax, workspace, ws_bytes: int, stream=None) -> None:
+    _ok("mq_attention_paged_bf16", lib().mq_attention_paged_bf16(
+        _ptr(qkv), ldqkv, T, _ptr(cu_new), _ptr(ctx_lens), B, max_new, H, Hkv, D, _ptr(slots), _ptr(block_table),
+        max_pages, _ptr(k_pages), _ptr(v_pages), n_pages, page_size, _ptr(o), ldo, _ptr(o_amax), _ptr(workspace),
         ws_bytes, _stream(stream)))

@@ -757,6 +757,128 @@ mq_status mq_attention_decode_bf16(const void *qkv_bf16, int64_t m, int64_t pos0
                                                    S_max, o_bf16, workspace, stream));
 }
 
+namespace {
+
+bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool page_size_ok(int64_t ps) { return ps >= 8 && ps <= 256 && (ps & (ps - 1)) == 0; }
+
+// Sizes shared by the attention calls over many sequences.
+bool serving_sizes_ok(int64_t T, int64_t B, int64_t H, int64_t Hkv, int64_t D) {
+    return D == 128 && H >= 1 && Hkv >= 1 && H <= 1024 && H % Hkv == 0 && H / Hkv <= 128 && T >= 1 &&
+           T <= MQ_PAGED_MAX_TOKENS && B >= 1 && B <= MQ_PAGED_MAX_REQUESTS;
+}
+
+mq_status serving_attention(mq::PagedAttnArgs &a, int64_t page_size, bool have_pages, void *workspace,
+                            cudaStream_t stream) {
+    if (a.ldqkv % 8 != 0 || a.ldo % 8 != 0 || !aligned16(a.qkv) || !aligned16(a.o) || !aligned16(workspace) ||
+        !aligned_to(a.cu, 4) || !aligned_to(a.ctx, 4) || !aligned_to(a.slots, 8) || !aligned_to(a.table, 4) ||
+        !aligned_to(a.o_amax, 4) || !aligned16(a.k_pages) || !aligned16(a.v_pages))
+        return MQ_ERR_ALIGNMENT;
+    a.ps_shift = 0;
+    while (have_pages && (1 << a.ps_shift) < page_size) ++a.ps_shift;
+    DeviceInfo *d = nullptr;
+    mq_status st = device_info(&d);
+    if (st != MQ_OK) return st;
+    return cuda_status(mq::launch_attention_paged(a, workspace, d->err, d->num_sms, stream));
+}
+
+}  // namespace
+
+mq_status mq_paged_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
+                        const int32_t *free_pages, int64_t n_free, int32_t *block_table, int64_t max_pages,
+                        int64_t T, int32_t *cu_new, int64_t *slots, int32_t *info, cudaStream_t stream) {
+    if (!ctx_lens || !new_lens || !block_table || !cu_new || !slots || !info || n_free < 0 ||
+        (n_free > 0 && !free_pages))
+        return MQ_ERR_INVALID_ARG;
+    if (B < 1 || B > MQ_PAGED_MAX_REQUESTS || T < 1 || T > MQ_PAGED_MAX_TOKENS || !page_size_ok(page_size) ||
+        max_pages < 1 || max_pages > (1LL << 24) || n_free > INT32_MAX)
+        return MQ_ERR_SHAPE;
+    if (!aligned_to(ctx_lens, 4) || !aligned_to(new_lens, 4) || !aligned_to(free_pages, 4) ||
+        !aligned_to(block_table, 4) || !aligned_to(cu_new, 4) || !aligned_to(slots, 8) || !aligned_to(info, 4))
+        return MQ_ERR_ALIGNMENT;
+    DeviceInfo *d = nullptr;
+    mq_status st = device_info(&d);
+    if (st != MQ_OK) return st;
+    return cuda_status(mq::launch_paged_plan(ctx_lens, new_lens, B, page_size, free_pages, n_free, block_table,
+                                             max_pages, T, cu_new, slots, info, d->num_sms, stream));
+}
+
+size_t mq_attention_packed_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hkv, int64_t D) {
+    if (!serving_sizes_ok(T, B, H, Hkv, D)) return 0;
+    return mq::attention_paged_workspace_bytes(T, B, T, H, Hkv, false);
+}
+
+mq_status mq_attention_packed_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t T, const int32_t *cu_lens, int64_t B,
+                                   int64_t H, int64_t Hkv, int64_t D, const int64_t *slots, void *k_pages,
+                                   void *v_pages, int64_t n_pages, int64_t page_size, void *o_bf16, int64_t ldo,
+                                   float *o_amax, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!qkv_bf16 || !cu_lens || !o_bf16 || !workspace) return MQ_ERR_INVALID_ARG;
+    const bool cache = slots != nullptr;
+    if (cache != (k_pages != nullptr) || cache != (v_pages != nullptr)) return MQ_ERR_INVALID_ARG;
+    if (!serving_sizes_ok(T, B, H, Hkv, D) || ldqkv < (H + 2 * Hkv) * D || ldo < H * D) return MQ_ERR_SHAPE;
+    if (cache && (!page_size_ok(page_size) || n_pages < 1 || n_pages > INT32_MAX)) return MQ_ERR_SHAPE;
+    if (ws_bytes < mq_attention_packed_workspace_bytes(T, B, H, Hkv, D)) return MQ_ERR_INVALID_ARG;
+    mq::PagedAttnArgs a = {};
+    a.qkv = static_cast<const __nv_bfloat16 *>(qkv_bf16);
+    a.ldqkv = ldqkv;
+    a.cu = cu_lens;
+    a.slots = slots;
+    a.k_pages = static_cast<__nv_bfloat16 *>(k_pages);
+    a.v_pages = static_cast<__nv_bfloat16 *>(v_pages);
+    a.n_pages = cache ? n_pages : 0;
+    a.o = static_cast<__nv_bfloat16 *>(o_bf16);
+    a.ldo = ldo;
+    a.o_amax = o_amax;
+    a.T = static_cast<int>(T);
+    a.B = static_cast<int>(B);
+    a.max_new = static_cast<int>(T);
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    return serving_attention(a, page_size, cache, workspace, stream);
+}
+
+size_t mq_attention_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
+                                          int64_t D) {
+    if (!serving_sizes_ok(T, B, H, Hkv, D) || max_new < 1 || max_new > T) return 0;
+    return mq::attention_paged_workspace_bytes(T, B, max_new, H, Hkv, true);
+}
+
+mq_status mq_attention_paged_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t T, const int32_t *cu_new,
+                                  const int32_t *ctx_lens, int64_t B, int64_t max_new, int64_t H, int64_t Hkv,
+                                  int64_t D, const int64_t *slots, const int32_t *block_table, int64_t max_pages,
+                                  void *k_pages, void *v_pages, int64_t n_pages, int64_t page_size, void *o_bf16,
+                                  int64_t ldo, float *o_amax, void *workspace, size_t ws_bytes,
+                                  cudaStream_t stream) {
+    if (!qkv_bf16 || !cu_new || !ctx_lens || !block_table || !k_pages || !v_pages || !o_bf16 || !workspace)
+        return MQ_ERR_INVALID_ARG;
+    if (!serving_sizes_ok(T, B, H, Hkv, D) || max_new < 1 || max_new > T || ldqkv < (H + 2 * Hkv) * D ||
+        ldo < H * D || !page_size_ok(page_size) || n_pages < 1 || n_pages > INT32_MAX || max_pages < 1 ||
+        max_pages > (1LL << 24))
+        return MQ_ERR_SHAPE;
+    if (ws_bytes < mq_attention_paged_workspace_bytes(T, B, max_new, H, Hkv, D)) return MQ_ERR_INVALID_ARG;
+    mq::PagedAttnArgs a = {};
+    a.qkv = static_cast<const __nv_bfloat16 *>(qkv_bf16);
+    a.ldqkv = ldqkv;
+    a.cu = cu_new;
+    a.ctx = ctx_lens;
+    a.slots = slots;
+    a.table = block_table;
+    a.max_pages = static_cast<int>(max_pages);
+    a.k_pages = static_cast<__nv_bfloat16 *>(k_pages);
+    a.v_pages = static_cast<__nv_bfloat16 *>(v_pages);
+    a.n_pages = n_pages;
+    a.o = static_cast<__nv_bfloat16 *>(o_bf16);
+    a.ldo = ldo;
+    a.o_amax = o_amax;
+    a.T = static_cast<int>(T);
+    a.B = static_cast<int>(B);
+    a.max_new = static_cast<int>(max_new);
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    return serving_attention(a, page_size, true, workspace, stream);
+}
+
 mq_status mq_decode_linear_bf16(const mq_weight *w, const void *x_bf16, int64_t M, void *y_bf16,
                                 cudaStream_t stream) {
     if (!x_bf16 || !y_bf16) return MQ_ERR_INVALID_ARG;

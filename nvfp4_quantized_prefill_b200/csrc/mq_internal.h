@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 #include <utility>
@@ -118,6 +119,33 @@ int attention_decode_max_rows();
 cudaError_t launch_attention_decode(const void *qkv, int64_t m, int64_t pos0, int64_t H, int64_t Hkv,
                                     void *k_cache, void *v_cache, int64_t S_max, void *o, void *ws,
                                     cudaStream_t s);
+
+// ---- paged serving (mq_paged_plan.cu, mq_attention_paged.cu) -------------------
+
+// Pages and slots of a step's new tokens; see mq_paged_plan.
+cudaError_t launch_paged_plan(const int *ctx, const int *nw, int64_t B, int64_t page_size, const int *free_pages,
+                              int64_t n_free, int *table, int64_t max_pages, int64_t T, int *cu, int64_t *slots,
+                              int *info, int num_sms, cudaStream_t s);
+
+// A step's attention over many sequences.  table NULL: keys and values are the
+// batch's own rows (packed prompts); else those of the paged cache.
+struct PagedAttnArgs {
+    const __nv_bfloat16 *qkv;      // [T, (H + 2 Hkv) * 128], leading dimension ldqkv
+    int64_t ldqkv;
+    const int *cu;                 // [B + 1] first row of each sequence
+    const int *ctx;                // [B] tokens cached before the step (NULL with packed prompts)
+    const int64_t *slots;          // [T] cache slot of each row, NULL: no cache write
+    const int *table;              // [B, max_pages]
+    __nv_bfloat16 *k_pages;        // [n_pages, Hkv, page size, 128]
+    __nv_bfloat16 *v_pages;
+    int64_t n_pages;
+    __nv_bfloat16 *o;              // [T, H * 128], leading dimension ldo
+    int64_t ldo;
+    float *o_amax;                 // receives max |o|, or NULL
+    int T, B, max_new, H, Hkv, max_pages, ps_shift;
+};
+size_t attention_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv, bool paged);
+cudaError_t launch_attention_paged(const PagedAttnArgs &a, void *ws, unsigned *err, int num_sms, cudaStream_t s);
 
 // ---- decode (mq_decode.cu: BF16; mq_decode_nvf4.cu: NVFP4 W4A4) ----------------
 
