@@ -343,7 +343,8 @@ mq_status mq_attention_decode_bf16(const void *qkv_bf16, int64_t m, int64_t pos0
  * pages its row of block_table (device int32 [B, max_pages]) names: position
  * p lies in page block_table[b][p / page_size], and slot s (int64) means row
  * s % page_size of page s / page_size.  page_size is a power of two from 8 to
- * 256.  A step's new tokens are packed: those of sequence b are rows
+ * 256; n_pages * Hkv * page_size stays below 2^34 rows and max_pages *
+ * page_size within 2^30 positions.  A step's new tokens are packed: those of sequence b are rows
  * cu[b] .. cu[b + 1] - 1 of the batch (device int32 [B + 1], ascending, from
  * 0; a sequence may have none), and rows from cu[B] on (padding up to T) are
  * neither read nor written.  All lengths, tables and slots are read on the

@@ -1,13 +1,38 @@
 // mq_attention_paged.cu -- attention of a serving step over many sequences at
 // once: packed prompts (keys and values in the batch itself) and new tokens
-// over a paged KV cache.
+// over a paged KV cache (BF16 in and out, FP32 softmax and accumulation).
 //
 //   o[t, h, :] = sum_{j <= pos(t)} softmax_j( q[t,h,:] . k[j,g,:] / sqrt(D) ) v[j,g,:],
 //   g = h / (H / Hkv), j over the positions of t's own sequence.
 //
-// One warp per (token, query head): each lane holds four of the 128
-// dimensions, keys are taken one after the other with a running maximum and
-// sum in FP32.
+// Rows of a tile.  The H / Hkv = G query heads of a KV head read the same keys,
+// so a 128-row tile holds R = 128 / G tokens times G heads (one TMA box takes
+// them out of the batch in that order): the keys cross shared memory once for
+// all of them, and a causal tile wastes at most R + 127 positions.
+//
+// One persistent CTA per SM with two slots, each a 128-row tile with its own
+// S / P (128 columns of tensor memory; P in BF16 over S) and O (128 columns):
+// while one slot's softmax runs, the tensor cores work for the other.  An item
+// of work is 2 R tokens of a sequence and a KV head: slot 0 takes the first R
+// tokens, slot 1 the others, both over the same K / V tiles.  An item of at
+// most R tokens (single tokens, draft tokens, the rest of a chunk) gives both
+// slots the same queries and every other K / V tile; their two results are
+// merged in the epilogue, so a decode step keeps two tiles in flight too.
+//
+// Warps: 0-3 / 4-7 softmax of slot 0 / 1 (a thread per row), 8-11 epilogue,
+// 12 / 13 MMA issue of slot 0 / 1, 14 work list and TMA, 15 cleans V tiles.
+//
+// Cleaning: P is 0 at a masked key, but 0 x NaN is NaN, and what lies behind a
+// sequence's last key (unwritten cache rows, another sequence, padding) may be
+// anything.  V rows past the item's last key are zeroed in shared memory; a
+// non-finite value of a new token (visible to some rows of the tile, masked
+// for others) is zeroed too and added again, row by row, in the epilogue.
+//
+// Work.  Packed prompts: items sorted by length, heaviest first, all items of a
+// head together (its keys stay in L2), taken from a counter.  Paged: the K / V
+// tiles of all items in a row, cut into one equal range per CTA; an item cut
+// by a border leaves (max, sum, unnormalised o) of its parts, merged by a
+// second kernel, so one long sequence fills the GPU as well as many do.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -21,112 +46,1133 @@ namespace mq {
 namespace {
 
 constexpr int kD = 128;
+constexpr int kRows = 128;                          // rows of a slot's tile
+constexpr int kKeys = 128;                          // keys of a K / V tile
+constexpr uint32_t kTileBytes = 128 * kD * 2;       // 32 KB: a Q, K or V tile
+constexpr int kRing = 5;                            // K / V tiles in flight or in use
+constexpr int kWork = 2;                            // items known ahead
+constexpr uint32_t kQOff = 0;                       // a Q tile per slot
+constexpr uint32_t kRingOff = 2 * kTileBytes;
+constexpr uint32_t kStatOff = kRingOff + kRing * kTileBytes;     // [2 slots][max, sum][128] floats
+constexpr uint32_t kWorkOff = kStatOff + 2 * 2 * kRows * 4;      // [kWork] items
+constexpr uint32_t kBarOff = kWorkOff + kWork * 64;
+constexpr uint32_t kSmemBytes = kBarOff + 544;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;                 // S0, S1, O0, O1
+constexpr uint32_t kOCol = 256;
 // log2(e) / sqrt(128): scores in the base-2 exponent domain
 constexpr float kScaleLog2 = 0.12751743082459868f;
+constexpr float kRescaleThreshold = 8.0f;           // raise the running max past 2^8 growth only
 
-__device__ __forceinline__ int seq_of(const int *cu, int B, int t) {
-    int lo = 0, hi = B;
+// Barriers, 8 bytes each.  A wait names the parity of a phase, so it may only
+// be made by a warp that has seen every phase of that barrier before.  The
+// slots do not read the same K / V tiles (a dual item's take turns, a slot may
+// need one tile less), so a stage has a barrier for the tiles that both read
+// and one for those of either alone (sets 0, 1, 2).
+enum : uint32_t {
+    kBarWorkFull = 0,                       // [kWork]
+    kBarWorkEmpty = kBarWorkFull + kWork,   // [kWork]
+    kBarQFull = kBarWorkEmpty + kWork,      // [2]
+    kBarQEmpty = kBarQFull + 2,             // [2]
+    kBarKFull = kBarQEmpty + 2,             // [3][kRing] a K tile has landed
+    kBarVFull = kBarKFull + 3 * kRing,      // [kRing] a V tile has (seen by the cleaner)
+    kBarKvEmpty = kBarVFull + kRing,        // [kRing]
+    kBarClean = kBarKvEmpty + kRing,        // [3][kRing] the V tile may be read
+    kBarSFull = kBarClean + 3 * kRing,      // [2]
+    kBarPFull = kBarSFull + 2,              // [2]
+    kBarPvDone = kBarPFull + 2,             // [2] every P V product
+    kBarOFull = kBarPvDone + 2,             // [2] an item's last one
+    kBarOEmpty = kBarOFull + 2,             // [2]
+    kBarStatFull = kBarOEmpty + 2,          // [2]
+    kBarStatEmpty = kBarStatFull + 2,       // [2]
+    kBarDrain = kBarStatEmpty + 2,          // [2]
+    kBarCount = kBarDrain + 2
+};
+static_assert(kBarCount * 8 + 16 <= 544, "barriers, TMEM address and abort flag");
+
+// One entry of the work list: up to 2 R tokens of a sequence.
+struct Entry {
+    int row0;      // batch row of the first token
+    int ntok;
+    int pos0;      // its position
+    int kv;        // packed: batch row of position 0; paged: row of the block table
+};
+
+struct alignas(16) Item {
+    Entry e;
+    int g, t0, t1;       // KV head; K / V tiles [t0, t1) of it
+    int kv_len;          // keys from here on do not exist for this item
+    int c[2];            // tiles of each slot
+    int dual;            // both slots have the same queries and take turns at the tiles
+    int part;            // < 0: the whole item, write o; else the partial result's place
+    int last;            // no item: end of work
+    int bad;             // set by the cleaner: a new token's V is not finite
+};
+static_assert(sizeof(Item) <= 64, "work ring entry");
+
+struct Header {          // start of the workspace
+    int n_ent;
+    int counter;
+    int64_t tiles;       // K / V tiles of all entries (one head)
+};
+
+struct Params {
+    PagedAttnArgs a;
+    int R, G;            // tokens and heads of a tile
+    int max_ent;
+    Header *head;
+    Entry *ent;
+    int64_t *prefix;     // [n_ent + 1] tiles before each entry (paged)
+    float *part;         // [2 grid][part_rows](max, sum) then [part_rows][128]
+    int part_rows;
+    unsigned *err;
+};
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// box {64 columns, G heads, tokens, 1} of the queries
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// 128-byte-swizzled operand descriptor (see mq_ptx.cuh) with both byte offsets
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1u) << 46 |
+           static_cast<uint64_t>(2u) << 61;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Where a K / V tile's rows lie in shared memory: 8-row groups of 1 KB per
+// 64-column half.  Packed (one box of 128 rows per half): the groups of a half
+// lie together.  Paged (a box per page, [group][half][8 rows]): the halves of
+// a group lie together, so a page of any size lands in the same tile layout.
+template <bool kPaged>
+struct Layout {
+    static constexpr uint32_t kGroup = kPaged ? 2048 : 1024;
+    static constexpr uint32_t kHalf = kPaged ? 1024 : 16384;
+    // byte offset of 16-byte chunk c (0..15) of row k (128-byte swizzle)
+    __device__ static __forceinline__ uint32_t chunk(int k, int c) {
+        return (k >> 3) * kGroup + (c >> 3) * kHalf + (k & 7) * 128 + (((c & 7) ^ (k & 7)) << 4);
+    }
+};
+
+__device__ __forceinline__ int64_t range_begin(int64_t W, int c, int n) { return W * c / n; }
+
+// The entry that holds tile x of the head: the last e with prefix[e] <= x
+// (whole warp; 32 probes a step).
+__device__ __forceinline__ int find_entry(const int64_t *prefix, int n_ent, int64_t x, int lane) {
+    int lo = 0, hi = n_ent;                       // prefix[lo] <= x < prefix[hi]
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid; else hi = mid;
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + lane * step;
+        const bool le = i < hi && prefix[i] <= x;
+        const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, le));   // lane 0 always holds
+        const int nlo = lo + k * step;
+        hi = min(hi, nlo + step);
+        lo = nlo;
     }
     return lo;
 }
 
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 r = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
-                       __uint_as_float(r.y & 0xFFFF0000u));
+// V of a new token i of the entry (for the rows that a cleaned value belongs to)
+template <bool kPaged>
+__device__ const __nv_bfloat16 *new_value_row(const Params &p, const Item &w, int pos) {
+    if (!kPaged)
+        return p.a.qkv + static_cast<int64_t>(w.e.kv + pos) * p.a.ldqkv + (p.a.H + p.a.Hkv + w.g) * kD;
+    const int id = p.a.table[static_cast<int64_t>(w.e.kv) * p.a.max_pages + (pos >> p.a.ps_shift)];
+    if (id < 0 || id >= p.a.n_pages) return nullptr;
+    return p.a.v_pages +
+           (((static_cast<int64_t>(id) * p.a.Hkv + w.g) << p.a.ps_shift) + (pos & ((1 << p.a.ps_shift) - 1))) * kD;
 }
 
-// The new tokens' K and V rows to their slots (one warp per token and KV head:
-// 16 lanes for K, 16 for V).
-__global__ void __launch_bounds__(256) paged_append_kernel(const PagedAttnArgs p) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t n_slots = p.n_pages << p.ps_shift;
-    const int64_t total = static_cast<int64_t>(min(p.T, p.cu[p.B])) * p.Hkv;
-    const int lane = threadIdx.x & 31;
-    for (int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < total;
-         w += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
-        const int64_t t = w / p.Hkv, g = w % p.Hkv;
-        const int64_t slot = p.slots[t];
-        if (slot < 0 || slot >= n_slots) continue;
-        const int64_t dst = ((((slot >> p.ps_shift) * p.Hkv + g) << p.ps_shift) + (slot & ((1 << p.ps_shift) - 1))) * kD;
-        const __nv_bfloat16 *row = p.qkv + t * p.ldqkv + (p.H + g) * kD + (lane < 16 ? 0 : p.Hkv * kD);
-        reinterpret_cast<uint4 *>((lane < 16 ? p.k_pages : p.v_pages) + dst)[lane & 15] =
-            reinterpret_cast<const uint4 *>(row)[lane & 15];
-    }
-}
-
-__global__ void __launch_bounds__(256) paged_rows_kernel(const PagedAttnArgs p) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int total = max(min(p.T, p.cu[p.B]), 0);
-    const int group = p.H / p.Hkv, ps = 1 << p.ps_shift;
-    float amax = 0.0f;
-    for (int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-         w < static_cast<int64_t>(total) * p.H; w += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
-        const int t = static_cast<int>(w / p.H), h = static_cast<int>(w % p.H), g = h / group;
-        const int b = seq_of(p.cu, p.B, t);
-        const int start = max(p.cu[b], 0);
-        int64_t n = t - start + 1;           // keys of this row
-        if (p.table) n = min(n + max(p.ctx[b], 0), static_cast<int64_t>(p.max_pages) << p.ps_shift);
-        const float4 q = load4(p.qkv + t * p.ldqkv + h * kD + lane * 4);
-        float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t j = 0; j < n; ++j) {
-            const __nv_bfloat16 *k, *v;
-            if (p.table) {
-                const int id = p.table[static_cast<int64_t>(b) * p.max_pages + (j >> p.ps_shift)];
-                if (id < 0 || id >= p.n_pages) continue;
-                const int64_t off = (((static_cast<int64_t>(id) * p.Hkv + g) << p.ps_shift) + (j & (ps - 1))) * kD;
-                k = p.k_pages + off;
-                v = p.v_pages + off;
-            } else {
-                k = p.qkv + (start + j) * p.ldqkv + (p.H + g) * kD;
-                v = k + p.Hkv * kD;
-            }
-            const float4 kk = load4(k + lane * 4);
-            float s = q.x * kk.x + q.y * kk.y + q.z * kk.z + q.w * kk.w;
+// The new tokens' K and V rows to their slots, one warp per token and KV head
+// at a time (16 lanes for K, 16 for V), `n` warps in all.
+__device__ __forceinline__ void append_rows(const PagedAttnArgs &a, int64_t w, int64_t n, int lane) {
+    const int64_t n_slots = a.n_pages << a.ps_shift;
+    const int64_t total = static_cast<int64_t>(max(min(a.T, a.cu[a.B]), 0)) * a.Hkv;
+    constexpr int kU = 4;                          // rows in flight
+    for (; w < total; w += kU * n) {
+        uint4 v[kU];
+        int64_t dst[kU];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            s *= kScaleLog2;
-            const float mn = fmaxf(m, s), f = exp2f(m - mn), e = exp2f(s - mn);
-            const float4 vv = load4(v + lane * 4);
-            l = l * f + e;
-            a[0] = a[0] * f + e * vv.x;
-            a[1] = a[1] * f + e * vv.y;
-            a[2] = a[2] * f + e * vv.z;
-            a[3] = a[3] * f + e * vv.w;
-            m = mn;
+        for (int u = 0; u < kU; ++u) {
+            dst[u] = -1;
+            const int64_t x = w + u * n;
+            if (x >= total) continue;
+            const int64_t t = x / a.Hkv, g = x % a.Hkv;
+            const int64_t slot = a.slots[t];
+            if (slot < 0 || slot >= n_slots) continue;
+            dst[u] = ((((slot >> a.ps_shift) * a.Hkv + g) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * kD;
+            v[u] = reinterpret_cast<const uint4 *>(a.qkv + t * a.ldqkv + (a.H + g) * kD +
+                                                   (lane < 16 ? 0 : a.Hkv * kD))[lane & 15];
         }
-        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a row without keys: zeros; NaN stays
-        __nv_bfloat162 r[2] = {__floats2bfloat162_rn(a[0] * inv, a[1] * inv), __floats2bfloat162_rn(a[2] * inv, a[3] * inv)};
-        *reinterpret_cast<uint2 *>(p.o + t * p.ldo + h * kD + lane * 4) = *reinterpret_cast<uint2 *>(r);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            amax = fmaxf(amax, fmaxf(fabsf(__bfloat162float(r[i].x)), fabsf(__bfloat162float(r[i].y))));
+        for (int u = 0; u < kU; ++u)
+            if (dst[u] >= 0)
+                reinterpret_cast<uint4 *>((lane < 16 ? a.k_pages : a.v_pages) + dst[u])[lane & 15] = v[u];
     }
-    if (p.o_amax) {
+}
+
+// ---- the work list -----------------------------------------------------------------
+
+constexpr int kPrepThreads = 1024;
+constexpr int kBins = 4096;
+
+// Exclusive prefix sum over the block; *total gets the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *red, int64_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = red[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += y;
+        }
+        red[lane] = s;
+    }
+    __syncthreads();
+    *total = red[31];
+    const int64_t r = x - v + (warp ? red[warp - 1] : 0);
+    __syncthreads();
+    return r;
+}
+
+// Block 0 makes the work list; with a paged cache the other blocks meanwhile
+// write the new tokens' rows to it (packed prompts: the attention kernel does,
+// as nothing there reads the cache).
+template <bool kPaged>
+__global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p) {
+    extern __shared__ int offs[];                  // [B + 1] entries before each sequence; packed: then kBins bins
+    __shared__ int64_t red[32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const PagedAttnArgs &a = p.a;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (kPaged && blockIdx.x > 0) {
+        append_rows(a, static_cast<int64_t>(blockIdx.x - 1) * (kPrepThreads / 32) + (tid >> 5),
+                    static_cast<int64_t>(gridDim.x - 1) * (kPrepThreads / 32), lane);
+        return;
+    }
+    const int TB = 2 * p.R;
+    auto tokens = [&](int b) {                     // rows of sequence b, whatever cu holds
+        const int lo = min(max(a.cu[b], 0), a.T), hi = min(max(a.cu[b + 1], 0), a.T);
+        return min(max(hi - lo, 0), a.max_new);
+    };
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPrepThreads) {
+        const int b = b0 + tid;
+        int64_t total;
+        const int64_t at = block_scan(b < a.B ? (tokens(b) + TB - 1) / TB : 0, red, &total);
+        if (b < a.B) offs[b] = static_cast<int>(min(base + at, static_cast<int64_t>(p.max_ent)));
+        base += total;
+    }
+    const int n_ent = static_cast<int>(min(base, static_cast<int64_t>(p.max_ent)));
+    if (tid == 0) {
+        offs[a.B] = n_ent;
+        p.head->n_ent = n_ent;
+        p.head->counter = 0;
+        if (a.o_amax) *a.o_amax = 0.0f;
+    }
+    __syncthreads();
+    const int64_t cap = kPaged ? static_cast<int64_t>(a.max_pages) << a.ps_shift : INT32_MAX;
+    auto entry = [&](int e, int &tiles) {
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (offs[mid] <= e) lo = mid; else hi = mid;
+        }
+        const int first = (e - offs[lo]) * TB;
+        const int start = min(max(a.cu[lo], 0), a.T);
+        const int ctx = kPaged ? min(max(a.ctx[lo], 0), 1 << 30) : 0;
+        Entry r;
+        r.row0 = start + first;
+        r.ntok = min(tokens(lo) - first, TB);
+        r.pos0 = ctx + first;
+        r.kv = kPaged ? lo : start;
+        tiles = static_cast<int>((min(static_cast<int64_t>(r.pos0) + r.ntok, cap) + kKeys - 1) / kKeys);
+        return r;
+    };
+    if (kPaged) {
+        int64_t at0 = 0;
+        for (int e0 = 0; e0 < n_ent; e0 += kPrepThreads) {
+            const int e = e0 + tid;
+            int tiles = 0;
+            if (e < n_ent) p.ent[e] = entry(e, tiles);
+            int64_t total;
+            const int64_t at = block_scan(tiles, red, &total);
+            if (e < n_ent) p.prefix[e] = at0 + at;
+            at0 += total;
+        }
+        if (tid == 0) {
+            p.prefix[n_ent] = at0;
+            p.head->tiles = at0;
+        }
+    } else {
+        // counting sort by tiles, most first (the order within a bin does not
+        // matter: every item's result is its own)
+        int *bins = offs + a.B + 1;
+        for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
+        __syncthreads();
+        int shift = 0;
+        while (((a.T + kKeys - 1) / kKeys >> shift) >= kBins) ++shift;
+        for (int e = tid; e < n_ent; e += kPrepThreads) {
+            int tiles;
+            entry(e, tiles);
+            atomicAdd(&bins[kBins - 1 - (tiles >> shift)], 1);
+        }
+        __syncthreads();
+        constexpr int kPer = kBins / kPrepThreads;
+        int64_t sum = 0, total;
+        for (int i = 0; i < kPer; ++i) sum += bins[tid * kPer + i];
+        int64_t at = block_scan(sum, red, &total);
+        for (int i = 0; i < kPer; ++i) {
+            const int n = bins[tid * kPer + i];
+            bins[tid * kPer + i] = static_cast<int>(at);
+            at += n;
+        }
+        __syncthreads();
+        for (int e = tid; e < n_ent; e += kPrepThreads) {
+            int tiles;
+            const Entry r = entry(e, tiles);
+            p.ent[atomicAdd(&bins[kBins - 1 - (tiles >> shift)], 1)] = r;
+        }
+    }
+}
+
+// ---- the attention ---------------------------------------------------------------------
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                           const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using L = Layout<kPaged>;
+    const uint32_t s0 = smem_u32(smem);
+    const uint32_t bar = s0 + kBarOff;
+    auto B = [&](uint32_t i) { return bar + 8 * i; };
+    Item *items = reinterpret_cast<Item *>(smem + kWorkOff);
+    float *stat = reinterpret_cast<float *>(smem + kStatOff);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kBarOff + kBarCount * 8);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + kBarOff + kBarCount * 8 + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.G, R = p.R;
+    unsigned *err = p.err;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWork; ++i) {
+            mbar_init(B(kBarWorkFull + i), 1);
+            mbar_init(B(kBarWorkEmpty + i), 8 + 4 + 2 + 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(B(kBarVFull + i), 1);
+            mbar_init(B(kBarKvEmpty + i), 2);
+        }
+        for (int i = 0; i < 3 * kRing; ++i) {
+            mbar_init(B(kBarKFull + i), 1);
+            mbar_init(B(kBarClean + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B(kBarQFull + i), 1);
+            mbar_init(B(kBarQEmpty + i), 1);
+            mbar_init(B(kBarSFull + i), 1);
+            mbar_init(B(kBarPFull + i), 4);
+            mbar_init(B(kBarPvDone + i), 1);
+            mbar_init(B(kBarOFull + i), 1);
+            mbar_init(B(kBarOEmpty + i), 4);
+            mbar_init(B(kBarStatFull + i), 4);
+            mbar_init(B(kBarStatEmpty + i), 4);
+            mbar_init(B(kBarDrain + i), 1);
+        }
+        fence_barrier_init();
+        *abort = (s0 & 1023u) != 0;          // the tiles' swizzle needs 1 KB alignment
+        if (s0 & 1023u) atomicOr(err, kDevErrTimeout);
+        prefetch_tmap(&tmap_q);
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+    }
+    if (warp == 12) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+    const bool dead = *abort != 0;
+
+    auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait(b, parity, abort, err); };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        regs_inc<192>();
+        const int s = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + s * 128u;
+        const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kOCol + s * 128u;
+        const int tok_r = r / G;
+        uint32_t n_s = 0;                       // S tiles of this slot so far
+        bool ok = !dead;
+        for (uint32_t it = 0; ok; ++it) {
+            const uint32_t wi = it % kWork;
+            ok = __all_sync(0xFFFFFFFFu, wait(B(kBarWorkFull + wi), (it / kWork) & 1));
+            if (!ok || items[wi].last) break;
+            const Item &w = items[wi];
+            const int dual = w.dual, c = w.c[s], t0 = w.t0;
+            const int first = dual ? 0 : s * R;                  // the slot's first token
+            const int mine = first + tok_r;
+            const bool valid = r < R * G && mine < w.e.ntok;
+            const int lim = min(w.e.pos0 + mine, w.kv_len - 1);  // the last key of this row
+            const int free_to = min(w.e.pos0 + first, w.kv_len - 1);   // every row of the slot sees keys up to here
+            const bool busy = __any_sync(0xFFFFFFFFu, valid);
+            float m = -INFINITY, l = 0.0f;
+            for (int i = 0; i < c; ++i, ++n_s) {
+                const int j = dual ? t0 + s + 2 * i : t0 + i;
+                ok = __all_sync(0xFFFFFFFFu, wait(B(kBarSFull + s), n_s & 1));
+                if (!ok) break;
+                if (!busy) {                    // no row of this warp is in the item: P may be anything
+                    if (lane == 0) mbar_arrive(B(kBarPFull + s));
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t sr[128];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tmem_ld32(tS + 32u * h, *reinterpret_cast<uint32_t (*)[32]>(&sr[32 * h]));
+                tmem_ld_wait();
+                float *sf = reinterpret_cast<float *>(sr);
+                if (j * kKeys + kKeys - 1 > free_to) {
+                    const int last = lim - j * kKeys;
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (k > last) sf[k] = -INFINITY;
+                }
+                float mp[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mp[e] = fmaxf(sf[e], sf[8 + e]);
+#pragma unroll
+                for (int k = 16; k < 128; k += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mp[e] = fmax3(mp[e], sf[k + e], sf[k + 8 + e]);
+                const float mx =
+                    fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], fmax3(mp[5], mp[6], mp[7]))) * kScaleLog2;
+                // the maximum is raised only for a growth beyond 2^8 (weights
+                // stay below 2^8, the sum is taken to the same base)
+                const bool need = valid && mx > m + kRescaleThreshold;
+                if (__any_sync(0xFFFFFFFFu, need)) {
+                    const float mn = need ? mx : m;
+                    const float f = need ? exp2f(m - mn) : 1.0f;
+                    if (i > 0) {
+                        ok = __all_sync(0xFFFFFFFFu, wait(B(kBarPvDone + s), (n_s - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            uint32_t ov[16];
+                            tmem_ld16(tO + 16u * q, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+                            tmem_st16(tO + 16u * q, ov);
+                        }
+                    }
+                    l *= f;
+                    m = mn;
+                }
+                const float nm = m == -INFINITY ? 0.0f : -m;     // no key seen yet: every weight is 2^-inf = 0
+                const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), nm2 = pack2(nm, nm);
+                uint64_t lp[2] = {0, 0};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float x0, x1;
+                        unpack2(ffma2(pack2(sf[32 * h + 2 * k], sf[32 * h + 2 * k + 1]), sc2, nm2), x0, x1);
+                        x0 = ex2_approx(x0);
+                        x1 = ex2_approx(x1);
+                        lp[k & 1] = fadd2(lp[k & 1], pack2(x0, x1));
+                        const __nv_bfloat162 pb = __floats2bfloat162_rn(x0, x1);
+                        pk[k] = *reinterpret_cast<const uint32_t *>(&pb);
+                    }
+                    tmem_st16(tS + 16u * h, pk);
+                }
+                float a0, a1;
+                unpack2(fadd2(lp[0], lp[1]), a0, a1);
+                l += a0 + a1;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B(kBarPFull + s));
+            }
+            if (!ok) break;
+            ok = __all_sync(0xFFFFFFFFu, it == 0 || wait(B(kBarStatEmpty + s), (it - 1) & 1));
+            if (!ok) break;
+            stat[s * 256 + r] = m;
+            stat[s * 256 + 128 + r] = l;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(B(kBarStatFull + s));
+                mbar_arrive(B(kBarWorkEmpty + wi));
+            }
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ epilogue
+        regs_dec<80>();
+        const int quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kOCol;
+        if (!kPaged && p.a.slots && !dead)
+            append_rows(p.a, static_cast<int64_t>(blockIdx.x) * 4 + quarter, static_cast<int64_t>(gridDim.x) * 4, lane);
+        float amax = 0.0f;
+        uint32_t n_o[2] = {0, 0};               // items with tiles in each slot
+        bool ok = !dead;
+        for (uint32_t it = 0; ok; ++it) {
+            const uint32_t wi = it % kWork;
+            ok = __all_sync(0xFFFFFFFFu, wait(B(kBarWorkFull + wi), (it / kWork) & 1));
+            if (!ok || items[wi].last) break;
+            const Item &w = items[wi];
+            for (int s = 0; s < 2 && ok; ++s) {
+                // both slots of a dual item are finished in one turn
+                const bool both = w.dual != 0;
+                if (both && s == 1) break;
+                for (int q = s; q < (both ? 2 : s + 1) && ok; ++q) {
+                    ok = __all_sync(0xFFFFFFFFu, wait(B(kBarStatFull + q), it & 1));
+                    if (ok && w.c[q]) ok = __all_sync(0xFFFFFFFFu, wait(B(kBarOFull + q), n_o[q]++ & 1));
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const int tok = (both ? 0 : s * R) + r / G;
+                const bool valid = r < R * G && tok < w.e.ntok;
+                const int pos = w.e.pos0 + tok;
+                float m = stat[s * 256 + r], l = stat[s * 256 + 128 + r];
+                float f0 = 1.0f, f1 = 0.0f;
+                if (both) {
+                    const float m1 = stat[256 + r], l1 = stat[256 + 128 + r];
+                    const float mm = fmaxf(m, m1);
+                    if (mm > -INFINITY) {
+                        f0 = m > -INFINITY ? exp2f(m - mm) : 0.0f;
+                        f1 = m1 > -INFINITY ? exp2f(m1 - mm) : 0.0f;
+                    }
+                    // (a NaN sum stays one)
+                    l = l * f0 + l1 * f1;
+                    m = mm;
+                }
+                const bool two = both && w.c[1] > 0;
+                const bool one = w.c[s] > 0;
+                const float inv = w.part >= 0 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);   // no key: zeros
+                const int prow = (both ? 0 : s * kRows) + r;
+                float *pm = nullptr, *po = nullptr;
+                if (w.part >= 0) {
+                    float *base = p.part + static_cast<int64_t>(w.part) * p.part_rows * (2 + kD);
+                    pm = base + prow * 2;
+                    po = base + p.part_rows * 2 + static_cast<int64_t>(prow) * kD;
+                    if (valid) {
+                        pm[0] = m;
+                        pm[1] = l;
+                    }
+                }
+                __nv_bfloat16 *orow = p.a.o + static_cast<int64_t>(w.e.row0 + tok) * p.a.ldo + (w.g * G + r % G) * kD;
+                const int bad = w.bad;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t ov[16];
+                    float f[16];
+                    if (one) {
+                        tmem_ld16(tO + s * 128u + 16u * c, ov);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(ov[e]) * f0;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[e] = 0.0f;
+                    }
+                    if (two) {
+                        tmem_ld16(tO + 128u + 16u * c, ov);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(ov[e]), f1, f[e]);
+                    }
+                    if (bad && valid) {
+                        // cleaned values of the keys this row does see
+                        for (int k = max(w.e.pos0 + 1, w.t0 * kKeys); k <= min(min(pos, w.kv_len - 1), w.t1 * kKeys - 1); ++k) {
+                            const __nv_bfloat16 *v = new_value_row<kPaged>(p, w, k);
+                            if (!v) continue;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float x = __bfloat162float(v[16 * c + e]);
+                                if (!isfinite(x)) f[e] += x;
+                            }
+                        }
+                    }
+                    if (valid && w.part >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<float4 *>(po + 16 * c)[e] =
+                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else if (valid) {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e] * inv, f[2 * e + 1] * inv);
+                            amax = fmaxf(amax, fmaxf(fabsf(__bfloat162float(b.x)), fabsf(__bfloat162float(b.y))));
+                            pk[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        reinterpret_cast<uint4 *>(orow + 16 * c)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        reinterpret_cast<uint4 *>(orow + 16 * c)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    for (int q = s; q < (both ? 2 : s + 1); ++q) {
+                        mbar_arrive(B(kBarStatEmpty + q));
+                        if (w.c[q]) mbar_arrive(B(kBarOEmpty + q));
+                    }
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(B(kBarWorkEmpty + wi));
+        }
+        if (p.a.o_amax) {
+            const unsigned u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
+            if (lane == 0 && u) atomicMax(reinterpret_cast<unsigned *>(p.a.o_amax), u);
+        }
+    } else {
+        regs_dec<48>();
+        if (warp < 14) {
+            // -------------------------------------------------------- MMA issue of one slot
+            if (lane == 0) {
+                const int s = warp - 12;
+                const uint32_t tS = tmem + s * 128u, tO = tmem + kOCol + s * 128u;
+                constexpr uint32_t idesc_s = idesc_bf16(128, 128, 0, 0);
+                constexpr uint32_t idesc_o = idesc_bf16(128, 128, 0, 1);   // V MN-major
+                const uint64_t qd = sdesc_sw128(s0 + kQOff + s * kTileBytes, 16, 1024);
+                uint32_t n_kv = 0;              // K / V pairs before this item
+                uint32_t n_s = 0, n_q = 0;      // tiles and items of this slot
+                uint32_t k_par = 0, v_par = 0;  // parity of each barrier's next phase
+                bool ok = !dead;
+                for (uint32_t it = 0; ok; ++it) {
+                    const uint32_t wi = it % kWork;
+                    ok = wait(B(kBarWorkFull + wi), (it / kWork) & 1);
+                    if (!ok || items[wi].last) break;
+                    const Item &w = items[wi];
+                    const int n = w.t1 - w.t0, c = w.c[s], other = w.c[s ^ 1], dual = w.dual;
+                    mbar_arrive(B(kBarWorkEmpty + wi));
+                    if (c) {
+                        ok = wait(B(kBarQFull + s), n_q & 1);
+                        for (int i = 0; i < c && ok; ++i, ++n_s) {
+                            const int jj = dual ? s + 2 * i : i;
+                            const uint32_t ki = 2 * (n_kv + jj), vi = ki + 1;
+                            const uint32_t ks = ki % kRing, vs = vi % kRing;
+                            // a tile that only this slot reads is released by it alone
+                            const bool alone = dual || i >= other;
+                            const uint32_t set = alone ? (1 + s) * kRing : 0;
+                            ok = wait(B(kBarKFull + set + ks), (k_par >> (set + ks)) & 1);
+                            k_par ^= 1u << (set + ks);
+                            if (!ok) break;
+                            tc_fence_after();
+                            // S = Q K^T (P of the tile before was read by an
+                            // earlier product of this thread: in order)
+                            const uint64_t kd = sdesc_sw128(s0 + kRingOff + ks * kTileBytes, 16, L::kGroup);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_ss(tS, qd + (k >> 2) * 1024 + (k & 3) * 2, kd + (k >> 2) * (L::kHalf >> 4) + (k & 3) * 2,
+                                       idesc_s, k > 0);
+                            tc_commit(B(kBarSFull + s));
+                            tc_commit(B(kBarKvEmpty + ks));
+                            if (alone) tc_commit(B(kBarKvEmpty + ks));
+                            if (i == c - 1) tc_commit(B(kBarQEmpty + s));
+                            if (i == 0 && n_q > 0) ok = wait(B(kBarOEmpty + s), (n_q - 1) & 1);
+                            ok = ok && wait(B(kBarPFull + s), n_s & 1) &&
+                                 wait(B(kBarClean + set + vs), (v_par >> (set + vs)) & 1);
+                            v_par ^= 1u << (set + vs);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t vd = sdesc_sw128(s0 + kRingOff + vs * kTileBytes, L::kHalf, L::kGroup);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_ts(tO, tS + 8 * k, vd + k * (2 * L::kGroup >> 4), idesc_o, i > 0 || k > 0);
+                            tc_commit(B(kBarPvDone + s));
+                            tc_commit(B(kBarKvEmpty + vs));
+                            if (alone) tc_commit(B(kBarKvEmpty + vs));
+                            if (i == c - 1) tc_commit(B(kBarOFull + s));
+                        }
+                        ++n_q;
+                    }
+                    n_kv += n;
+                }
+                // every MMA issued completes before tensor memory is freed
+                tc_commit(B(kBarDrain + s));
+                mbar_wait_plain(B(kBarDrain + s), 0);
+            }
+            __syncwarp();
+        } else if (warp == 14) {
+            // -------------------------------------------------------- work list and loads
+            const PagedAttnArgs &a = p.a;
+            const int n_ent = p.head->n_ent;
+            const int64_t tiles = kPaged ? p.head->tiles : 0;
+            const int64_t W = tiles * a.Hkv;
+            const int grid = static_cast<int>(kPaged ? (W < gridDim.x ? W : gridDim.x) : gridDim.x);
+            int64_t at = 0, end = 0;
+            int g = 0, e = 0;
+            if (tiles > 0 && static_cast<int>(blockIdx.x) < grid) {
+                at = range_begin(W, blockIdx.x, grid);
+                end = range_begin(W, blockIdx.x + 1, grid);
+                g = static_cast<int>(at / max(tiles, static_cast<int64_t>(1)));
+                e = find_entry(p.prefix, n_ent, at - g * tiles, lane);
+            }
+            const int64_t cap = kPaged ? static_cast<int64_t>(a.max_pages) << a.ps_shift : INT32_MAX;
+            const int page_rows = min(1 << a.ps_shift, kKeys);
+            const int n_groups = page_rows / 8;                        // 8-row groups of a box
+            const int boxes = kPaged ? kKeys / page_rows : 1;          // boxes of a tile
+            const int oob = static_cast<int>((a.n_pages * a.Hkv) << a.ps_shift >> 3);   // behind the last group
+            const int q_tok = min(R, a.max_new);
+            uint32_t n_kv = 0, n_q[2] = {0, 0};
+            uint32_t used = 0, par = 0;          // full barriers (K sets, then V) and the parity of their last phase
+            bool ok = !dead;
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t wi = it % kWork;
+                // the next item
+                Item w = {};
+                w.last = 1;
+                if (kPaged) {
+                    if (at < end) {
+                        // (entries without tiles are passed over)
+                        int64_t pe;
+                        while ((pe = p.prefix[e + 1]) <= at - g * tiles) {
+                            if (++e == n_ent) {
+                                e = 0;
+                                ++g;
+                            }
+                        }
+                        const int64_t pb = p.prefix[e], x = at - g * tiles;
+                        w.e = p.ent[e];
+                        w.g = g;
+                        w.last = 0;
+                        w.t0 = static_cast<int>(x - pb);
+                        const int64_t stop = min(pe - pb, w.t0 + (end - at));
+                        w.t1 = static_cast<int>(stop);
+                        const int place = 2 * static_cast<int>(blockIdx.x);
+                        w.part = w.t0 > 0 ? place : (stop < pe - pb ? place + 1 : -1);
+                        at += w.t1 - w.t0;
+                    }
+                } else {
+                    int idx = 0;
+                    if (lane == 0) idx = atomicAdd(&p.head->counter, 1);
+                    idx = __shfl_sync(0xFFFFFFFFu, idx, 0);
+                    if (n_ent > 0 && idx < static_cast<int64_t>(n_ent) * a.Hkv) {
+                        w.e = p.ent[idx % n_ent];
+                        w.g = idx / n_ent;
+                        w.last = 0;
+                        w.t1 = (w.e.pos0 + w.e.ntok + kKeys - 1) / kKeys;
+                        w.part = -1;
+                    }
+                }
+                if (!w.last) {
+                    w.kv_len = static_cast<int>(min(static_cast<int64_t>(w.e.pos0) + w.e.ntok, cap));
+                    w.dual = w.e.ntok <= R;
+                    const int n = w.t1 - w.t0;
+                    if (w.dual) {
+                        w.c[0] = (n + 1) / 2;
+                        w.c[1] = n / 2;
+                    } else {
+                        const int e0 = (min(w.e.pos0 + R, w.kv_len) + kKeys - 1) / kKeys;
+                        w.c[0] = max(min(e0, w.t1) - w.t0, 0);
+                        w.c[1] = n;
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, it < kWork || wait(B(kBarWorkEmpty + wi), ((it / kWork) - 1) & 1));
+                if (!ok) break;
+                if (lane == 0) {
+                    items[wi] = w;
+                    mbar_arrive(B(kBarWorkFull + wi));
+                }
+                if (w.last) break;
+                // its loads: the first K / V pair, the queries, the other pairs
+                const int n = w.t1 - w.t0;
+                const int *trow = kPaged ? a.table + static_cast<int64_t>(w.e.kv) * a.max_pages : nullptr;
+                auto page_of = [&](int j) {         // coordinate of this lane's box of tile j, or -1: nothing to load
+                    if (!kPaged) return 0;
+                    const int64_t pos = static_cast<int64_t>(j) * kKeys + lane * page_rows;
+                    if (lane >= boxes || pos >= w.kv_len) return -1;
+                    const int id = trow[pos >> a.ps_shift];
+                    if (id < 0 || id >= a.n_pages) return oob;
+                    return static_cast<int>((static_cast<int64_t>(id) * a.Hkv + w.g) << a.ps_shift >> 3) +
+                           (static_cast<int>(pos & ((1 << a.ps_shift) - 1)) >> 3);
+                };
+                int coord = page_of(w.t0);
+                for (int jj = 0; jj < n && ok; ++jj) {
+                    const int next = jj + 1 < n ? page_of(w.t0 + jj + 1) : -1;
+                    const uint32_t n_box = kPaged ? __popc(__ballot_sync(0xFFFFFFFFu, coord >= 0)) : 1;
+                    const uint32_t bytes = kPaged ? n_box * n_groups * 2048u : kTileBytes;
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t idx = 2 * (n_kv + jj) + kv, st = idx % kRing;
+                        ok = __all_sync(0xFFFFFFFFu, idx < kRing || wait(B(kBarKvEmpty + st), ((idx / kRing) - 1) & 1));
+                        if (!ok) break;
+                        const uint32_t set = w.dual ? 1 + (jj & 1) : (jj < w.c[0] ? 0 : 2);
+                        const uint32_t fb = kv ? 3 * kRing + st : set * kRing + st;
+                        const uint32_t dst = s0 + kRingOff + st * kTileBytes, full = B(kBarKFull + fb);
+                        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                        par ^= (used >> fb & 1) << fb;
+                        used |= 1u << fb;
+                        __syncwarp();
+                        if (kPaged) {
+                            if (coord >= 0)
+                                tma_load_4d(dst + lane * (n_groups * 2048u), kv ? &tmap_v : &tmap_k, 0, 0, 0, coord, full);
+                        } else if (lane == 0) {
+                            tma_load_3d(dst, &tmap_k, 0, w.e.kv + (w.t0 + jj) * kKeys, 2 * (a.H + kv * a.Hkv + w.g), full);
+                        }
+                    }
+                    if (!ok) break;
+                    if (jj == 0) {
+                        for (int s = 0; s < 2 && ok; ++s) {
+                            if (!w.c[s]) continue;
+                            ok = __all_sync(0xFFFFFFFFu, n_q[s] == 0 || wait(B(kBarQEmpty + s), (n_q[s] - 1) & 1));
+                            if (!ok) break;
+                            ++n_q[s];
+                            if (lane == 0) {
+                                const uint32_t dst = s0 + kQOff + s * kTileBytes, full = B(kBarQFull + s);
+                                const int row = w.e.row0 + (w.dual ? 0 : s * R);
+                                mbar_arrive_expect_tx(full, static_cast<uint32_t>(q_tok * G) * 256u);
+                                tma_load_4d(dst, &tmap_q, 0, w.g * G, row, 0, full);
+                                tma_load_4d(dst + 16384, &tmap_q, 0, w.g * G, row, 1, full);
+                            }
+                        }
+                    }
+                    coord = next;
+                }
+                n_kv += n;
+            }
+            if (!ok) {
+                // loads in flight land before the CTA may exit
+                for (uint32_t i = 0; i < 4 * kRing; ++i)
+                    if (used >> i & 1) mbar_wait_plain(B(kBarKFull + i), par >> i & 1);
+                for (int s = 0; s < 2; ++s)
+                    if (n_q[s]) mbar_wait_plain(B(kBarQFull + s), (n_q[s] - 1) & 1);
+            }
+        } else {
+            // -------------------------------------------------------- V tiles: clean and hand on
+            uint32_t n_kv = 0, v_par = 0;
+            bool ok = !dead;
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t wi = it % kWork;
+                ok = __all_sync(0xFFFFFFFFu, wait(B(kBarWorkFull + wi), (it / kWork) & 1));
+                if (!ok || items[wi].last) break;
+                const Item &w = items[wi];
+                const int dual = w.dual, c0 = w.c[0], t0 = w.t0, t1 = w.t1, kv_len = w.kv_len, from = min(w.e.pos0 + 1, kv_len);
+                for (int j = t0; j < t1 && ok; ++j) {
+                    const uint32_t vi = 2 * (n_kv + j - t0) + 1, vs = vi % kRing;
+                    ok = __all_sync(0xFFFFFFFFu, wait(B(kBarVFull + vs), v_par >> vs & 1));
+                    if (!ok) break;
+                    v_par ^= 1u << vs;
+                    const int lo = max(from - j * kKeys, 0);       // rows some of the tile's queries do not see
+                    if (lo < kKeys) {
+                        const uint32_t tile = s0 + kRingOff + vs * kTileBytes;
+                        const int end = min(max(kv_len - j * kKeys, 0), kKeys);
+                        bool found = false;
+                        for (int i = min(lo, end) * 16 + lane; i < kKeys * 16; i += 32) {
+                            const uint32_t addr = tile + L::chunk(i >> 4, i & 15);
+                            if ((i >> 4) >= end) {
+                                st_shared_v4(addr, 0, 0, 0, 0);
+                                continue;
+                            }
+                            uint32_t v[4];
+                            ld_shared_v4(addr, v);
+                            bool any = false;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const bool lo_bad = (v[q] & 0x7F80u) == 0x7F80u, hi_bad = (v[q] & 0x7F800000u) == 0x7F800000u;
+                                if (lo_bad) v[q] &= 0xFFFF0000u;
+                                if (hi_bad) v[q] &= 0x0000FFFFu;
+                                any = any || lo_bad || hi_bad;
+                            }
+                            if (any) {
+                                st_shared_v4(addr, v[0], v[1], v[2], v[3]);
+                                found = true;
+                            }
+                        }
+                        if (__any_sync(0xFFFFFFFFu, found) && lane == 0) items[wi].bad = 1;
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    const int jj = j - t0;
+                    if (lane == 0) mbar_arrive(B(kBarClean + (dual ? 1 + (jj & 1) : (jj < c0 ? 0 : 2)) * kRing + vs));
+                }
+                if (!ok) break;
+                n_kv += t1 - t0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B(kBarWorkEmpty + wi));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---- parts of cut items -------------------------------------------------------------------
+
+constexpr int kCombineRows = 8;       // rows a block takes at a time: a warp each
+
+// Block (c, y): the item that begins in CTA c's range and goes on past it.
+// Its parts: c's second place, then the first place of the CTAs after c.
+__global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const Params p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PagedAttnArgs &a = p.a;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int n_ent = p.head->n_ent;
+    const int64_t tiles = p.head->tiles, W = tiles * a.Hkv;
+    const int grid = static_cast<int>(W < gridDim.x ? W : gridDim.x);
+    const int c = blockIdx.x;
+    if (c >= grid - 1) return;
+    const int64_t lo = range_begin(W, c, grid), hi = range_begin(W, c + 1, grid);
+    const int g = static_cast<int>((hi - 1) / tiles);
+    const int e = find_entry(p.prefix, n_ent, hi - 1 - g * tiles, lane);
+    const int64_t is = g * tiles + p.prefix[e], ie = g * tiles + p.prefix[e + 1];
+    if (is < lo || ie <= hi) return;
+    int last = c + 1;
+    while (range_begin(W, last + 1, grid) < ie) ++last;
+    const Entry en = p.ent[e];
+    const bool dual = en.ntok <= p.R;
+    const int64_t stride = static_cast<int64_t>(p.part_rows) * (2 + kD);
+    float amax = 0.0f;
+    const int rows = en.ntok * p.G;           // (token, head) pairs in order
+    for (int i = blockIdx.y * kCombineRows + warp; i < rows; i += gridDim.y * kCombineRows) {
+        const int tok = i / p.G, hh = i % p.G;
+        const int prow = dual || tok < p.R ? i : kRows + (tok - p.R) * p.G + hh;
+        const float *first = p.part + (2 * static_cast<int64_t>(c) + 1) * stride;
+        float m = -INFINITY;
+        for (int k = c + lane; k <= last; k += 32)
+            m = fmaxf(m, (k == c ? first : p.part + 2 * static_cast<int64_t>(k) * stride)[prow * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        float l = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = c; k <= last; ++k) {
+            const float *base = k == c ? first : p.part + 2 * static_cast<int64_t>(k) * stride;
+            const float2 ml = *reinterpret_cast<const float2 *>(base + prow * 2);
+            const float4 v = reinterpret_cast<const float4 *>(base + p.part_rows * 2 + static_cast<int64_t>(prow) * kD)[lane];
+            // (a part without a key for this row: maximum -inf, sum and o 0 or,
+            // where a value was not finite, that value)
+            const float f = ml.x > -INFINITY ? exp2f(ml.x - m) : 1.0f;
+            l = fmaf(ml.y, f, l);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+        reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(en.row0 + tok) * a.ldo + (g * p.G + hh) * kD)[lane] =
+            *reinterpret_cast<uint2 *>(r);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            amax = fmaxf(amax, fmaxf(fabsf(__bfloat162float(r[q].x)), fabsf(__bfloat162float(r[q].y))));
+    }
+    if (a.o_amax) {
         const unsigned u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
-        if (lane == 0 && u) atomicMax(reinterpret_cast<unsigned *>(p.o_amax), u);
+        if (lane == 0 && u) atomicMax(reinterpret_cast<unsigned *>(a.o_amax), u);
     }
+}
+
+// ---- host -------------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = []() -> EncodeFn {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !ptr)
+            return nullptr;
+        return reinterpret_cast<EncodeFn>(ptr);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *m, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    EncodeFn fn = encode_fn();
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
+                    strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Workspace {
+    size_t ent, prefix, part, total;
+    int max_ent, part_rows;
+};
+
+Workspace carve(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv, bool paged, int num_sms) {
+    const int64_t G = H / Hkv, R = kRows / G;
+    Workspace w;
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    w.max_ent = static_cast<int>(T / (2 * R) + B);
+    w.ent = 256;
+    w.prefix = up(w.ent + sizeof(Entry) * w.max_ent);
+    w.part = paged ? up(w.prefix + sizeof(int64_t) * (w.max_ent + 1)) : w.prefix;
+    // (an even count keeps the 16-byte alignment of the rows behind the (max, sum) pairs)
+    w.part_rows = paged ? static_cast<int>(max_new <= R ? (max_new * G + 1) / 2 * 2 : 2 * kRows) : 0;
+    w.total = up(w.part + sizeof(float) * 2 * num_sms * w.part_rows * (2 + kD));
+    return w;
 }
 
 }  // namespace
 
+// (partial results for up to this many CTAs; the launch uses no more)
+constexpr int kMaxCtas = 160;
+
 size_t attention_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv, bool paged) {
-    return 256;
+    return carve(T, B, max_new, H, Hkv, paged, kMaxCtas).total;
+}
+
+template <bool kPaged>
+static cudaError_t launch_kind(Params &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
+                               cudaStream_t s) {
+    const PagedAttnArgs &a = p.a;
+    const size_t prep_smem = (a.B + 1 + (kPaged ? 0 : kBins)) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(paged_prep_kernel<kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kPagedMaxRequests + 1 + kBins) * static_cast<int>(sizeof(int)));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(paged_attention_kernel<kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    int prep_grid = 1;
+    if (kPaged && a.slots) {
+        const int64_t warps = static_cast<int64_t>(a.T) * a.Hkv;      // at most four rows a warp's turn
+        prep_grid += static_cast<int>(std::min<int64_t>((warps + 4 * 32 - 1) / (4 * 32), 2 * grid));
+    }
+    e = launch_pdl(paged_prep_kernel<kPaged>, dim3(prep_grid), dim3(kPrepThreads), prep_smem, s, p);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(paged_attention_kernel<kPaged>, dim3(grid), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    if (kPaged) {
+        const int y = (p.part_rows + kCombineRows - 1) / kCombineRows;
+        e = launch_pdl(paged_combine_kernel, dim3(grid, std::min(y, 8)), dim3(32 * kCombineRows), 0, s, p);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaGetLastError();
 }
 
 cudaError_t launch_attention_paged(const PagedAttnArgs &a, void *ws, unsigned *err, int num_sms, cudaStream_t s) {
-    cudaError_t e;
-    if (a.o_amax && (e = cudaMemsetAsync(a.o_amax, 0, sizeof(float), s)) != cudaSuccess) return e;
-    if (a.slots && (e = launch_pdl(paged_append_kernel, dim3(4 * num_sms), dim3(256), 0, s, a)) != cudaSuccess) return e;
-    const int64_t blocks = std::min<int64_t>((static_cast<int64_t>(a.T) * a.H + 7) / 8, 1 << 16);
-    e = launch_pdl(paged_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const bool paged = a.table != nullptr;
+    const int grid = std::min(num_sms, kMaxCtas);
+    const Workspace w = carve(a.T, a.B, a.max_new, a.H, a.Hkv, paged, kMaxCtas);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    Params p = {};
+    p.a = a;
+    p.G = a.H / a.Hkv;
+    p.R = kRows / p.G;
+    p.max_ent = w.max_ent;
+    p.head = reinterpret_cast<Header *>(base);
+    p.ent = reinterpret_cast<Entry *>(base + w.ent);
+    p.prefix = reinterpret_cast<int64_t *>(base + w.prefix);
+    p.part = reinterpret_cast<float *>(base + w.part);
+    p.part_rows = w.part_rows;
+    p.err = err;
+    CUtensorMap tq, tk, tv;
+    const cuuint64_t ld = static_cast<cuuint64_t>(a.ldqkv) * 2;
+    {
+        // queries as {64 columns, head, token, half}: a box is the G heads of a
+        // KV head for R tokens, token-major
+        const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(a.T), 2};
+        const cuuint64_t strides[3] = {kD * 2, ld, 128};
+        const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(std::min(p.R, a.max_new)), 1};
+        if (!encode(&tq, 4, a.qkv, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    if (paged) {
+        // pages as {64 columns, 8 rows, half, group of 8 rows}: a box is a page
+        // of one head (128 rows of it at most)
+        const cuuint64_t groups = static_cast<cuuint64_t>(a.n_pages * a.Hkv) << a.ps_shift >> 3;
+        const cuuint64_t dims[4] = {64, 8, 2, groups};
+        const cuuint64_t strides[3] = {kD * 2, 128, 2048};
+        const cuuint32_t box[4] = {64, 8, 2, static_cast<cuuint32_t>(std::min(1 << a.ps_shift, kKeys) / 8)};
+        if (!encode(&tk, 4, a.k_pages, dims, strides, box) || !encode(&tv, 4, a.v_pages, dims, strides, box))
+            return cudaErrorInvalidValue;
+        return launch_kind<true>(p, tq, tk, tv, grid, s);
+    }
+    // the batch's rows as {64 columns, row, 64-column block}
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(a.T), static_cast<cuuint64_t>(2 * (a.H + 2 * a.Hkv))};
+    const cuuint64_t strides[2] = {ld, 128};
+    const cuuint32_t box[3] = {64, kKeys, 2};
+    if (!encode(&tk, 3, a.qkv, dims, strides, box)) return cudaErrorInvalidValue;
+    return launch_kind<false>(p, tq, tk, tk, grid, s);
 }
 
 }  // namespace mq

@@ -769,6 +769,12 @@ bool serving_sizes_ok(int64_t T, int64_t B, int64_t H, int64_t Hkv, int64_t D) {
            T <= MQ_PAGED_MAX_TOKENS && B >= 1 && B <= MQ_PAGED_MAX_REQUESTS;
 }
 
+// (positions, and the cache counted in groups of 8 rows, are 32-bit on the device)
+bool cache_sizes_ok(int64_t n_pages, int64_t Hkv, int64_t page_size) {
+    return page_size_ok(page_size) && n_pages >= 1 && n_pages <= INT32_MAX &&
+           n_pages * Hkv <= (INT32_MAX - 256) / (page_size / 8);
+}
+
 mq_status serving_attention(mq::PagedAttnArgs &a, int64_t page_size, bool have_pages, void *workspace,
                             cudaStream_t stream) {
     if (a.ldqkv % 8 != 0 || a.ldo % 8 != 0 || !aligned16(a.qkv) || !aligned16(a.o) || !aligned16(workspace) ||
@@ -817,7 +823,7 @@ mq_status mq_attention_packed_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t 
     const bool cache = slots != nullptr;
     if (cache != (k_pages != nullptr) || cache != (v_pages != nullptr)) return MQ_ERR_INVALID_ARG;
     if (!serving_sizes_ok(T, B, H, Hkv, D) || ldqkv < (H + 2 * Hkv) * D || ldo < H * D) return MQ_ERR_SHAPE;
-    if (cache && (!page_size_ok(page_size) || n_pages < 1 || n_pages > INT32_MAX)) return MQ_ERR_SHAPE;
+    if (cache && !cache_sizes_ok(n_pages, Hkv, page_size)) return MQ_ERR_SHAPE;
     if (ws_bytes < mq_attention_packed_workspace_bytes(T, B, H, Hkv, D)) return MQ_ERR_INVALID_ARG;
     mq::PagedAttnArgs a = {};
     a.qkv = static_cast<const __nv_bfloat16 *>(qkv_bf16);
@@ -853,8 +859,8 @@ mq_status mq_attention_paged_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t T
     if (!qkv_bf16 || !cu_new || !ctx_lens || !block_table || !k_pages || !v_pages || !o_bf16 || !workspace)
         return MQ_ERR_INVALID_ARG;
     if (!serving_sizes_ok(T, B, H, Hkv, D) || max_new < 1 || max_new > T || ldqkv < (H + 2 * Hkv) * D ||
-        ldo < H * D || !page_size_ok(page_size) || n_pages < 1 || n_pages > INT32_MAX || max_pages < 1 ||
-        max_pages > (1LL << 24))
+        ldo < H * D || !cache_sizes_ok(n_pages, Hkv, page_size) || max_pages < 1 ||
+        max_pages > (1LL << 24) || max_pages > (1LL << 30) / page_size)
         return MQ_ERR_SHAPE;
     if (ws_bytes < mq_attention_paged_workspace_bytes(T, B, max_new, H, Hkv, D)) return MQ_ERR_INVALID_ARG;
     mq::PagedAttnArgs a = {};

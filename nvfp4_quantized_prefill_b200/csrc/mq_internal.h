@@ -129,6 +129,7 @@ cudaError_t launch_paged_plan(const int *ctx, const int *nw, int64_t B, int64_t 
 
 // A step's attention over many sequences.  table NULL: keys and values are the
 // batch's own rows (packed prompts); else those of the paged cache.
+constexpr int kPagedMaxRequests = 16384;
 struct PagedAttnArgs {
     const __nv_bfloat16 *qkv;      // [T, (H + 2 Hkv) * 128], leading dimension ldqkv
     int64_t ldqkv;
