@@ -56,7 +56,7 @@ constexpr uint32_t kRingOff = 2 * kTileBytes;
 constexpr uint32_t kStatOff = kRingOff + kRing * kTileBytes;     // [2 slots][max, sum][128] floats
 constexpr uint32_t kWorkOff = kStatOff + 2 * 2 * kRows * 4;      // [kWork] items
 constexpr uint32_t kBarOff = kWorkOff + kWork * 64;
-constexpr uint32_t kSmemBytes = kBarOff + 544;
+constexpr uint32_t kSmemBytes = kBarOff + 560;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;                 // S0, S1, O0, O1
@@ -65,8 +65,9 @@ constexpr uint32_t kOCol = 256;
 constexpr float kScaleLog2 = 0.12751743082459868f;
 constexpr float kRescaleThreshold = 8.0f;           // raise the running max past 2^8 growth only
 
-// Barriers, 8 bytes each.  A wait names the parity of a phase, so it may only
-// be made by a warp that has seen every phase of that barrier before.  The
+// Barriers, 8 bytes each.  A wait names the parity of a phase, so the phase
+// before must be known to be complete and the one after must not complete
+// until the wait is over.  The
 // slots do not read the same K / V tiles (a dual item's take turns, a slot may
 // need one tile less), so a stage has a barrier for the tiles that both read
 // and one for those of either alone (sets 0, 1, 2).
@@ -79,9 +80,9 @@ enum : uint32_t {
     kBarVFull = kBarKFull + 3 * kRing,      // [kRing] a V tile has (seen by the cleaner)
     kBarKvEmpty = kBarVFull + kRing,        // [kRing]
     kBarClean = kBarKvEmpty + kRing,        // [3][kRing] the V tile may be read
-    kBarSFull = kBarClean + 3 * kRing,      // [2]
-    kBarPFull = kBarSFull + 2,              // [2]
-    kBarPvDone = kBarPFull + 2,             // [2] every P V product
+    kBarSFull = kBarClean + 3 * kRing,      // [2 slots][2 halves]
+    kBarPFull = kBarSFull + 4,              // [2][2]
+    kBarPvDone = kBarPFull + 4,             // [2] every P V product
     kBarOFull = kBarPvDone + 2,             // [2] an item's last one
     kBarOEmpty = kBarOFull + 2,             // [2]
     kBarStatFull = kBarOEmpty + 2,          // [2]
@@ -89,7 +90,7 @@ enum : uint32_t {
     kBarDrain = kBarStatEmpty + 2,          // [2]
     kBarCount = kBarDrain + 2
 };
-static_assert(kBarCount * 8 + 16 <= 544, "barriers, TMEM address and abort flag");
+static_assert(kBarCount * 8 + 16 <= 560, "barriers, TMEM address and abort flag");
 
 // One entry of the work list: up to 2 R tokens of a sequence.
 struct Entry {
@@ -134,11 +135,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -156,6 +152,83 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// the three-input maximum that keeps a NaN
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Weights of 32 scores to the base 2^-nm as BF16 pairs, their sum (of the
+// unrounded weights) added to lp.
+__device__ __forceinline__ void weights32(const float *s, float nm, uint32_t (&pk)[16], uint64_t (&lp)[2]) {
+    const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), nm2 = pack2(nm, nm);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const uint64_t x = ffma2(pack2(s[2 * k], s[2 * k + 1]), sc2, nm2);
+        float y0, y1;
+        unpack2(x, y0, y1);
+        y0 = ex2_approx(y0);
+        y1 = ex2_approx(y1);
+        lp[k & 1] = fadd2(lp[k & 1], pack2(y0, y1));
+        const __nv_bfloat162 pb = __floats2bfloat162_rn(y0, y1);
+        pk[k] = *reinterpret_cast<const uint32_t *>(&pb);
+    }
+}
+
+// Bounded wait on a barrier's phase.  The first polls look at no clock: each
+// try_wait already suspends the warp for a while, and reading %globaltimer
+// after one failed poll cost more than the handover itself (with no product
+// and no softmax at all, the barriers alone took 1700 cycles a tile).
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort, unsigned *err) {
+    unsigned long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 127u) != 127u) continue;
+        if (*abort) return false;
+        const unsigned long long t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            atomicOr(err, kDevErrTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// (draining after the error is latched already)
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 32 lanes x 16 consecutive 32-bit columns into registers
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 // box {64 columns, G heads, tokens, 1} of the queries
@@ -181,18 +254,55 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
            static_cast<uint64_t>(2u) << 61;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Eight chained BF16 MMAs (K = 16 each) issued by one elected lane of a
+// converged warp: kept warp-wide so that the operands stay in uniform
+// registers (from a single-lane branch the same eight took ~1100 cycles).
+// D (+)= A B^T with A, B K-major; kHalfB: 16-byte units between B's column halves
+template <uint32_t kHalfB>
+__device__ __forceinline__ void warp_mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred e, f, t;\n\t"
+        ".reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+        "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
+        "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, %4;\n\t"
+        "add.s64 b5, %2, %5;\n\tadd.s64 b6, %2, %6;\n\tadd.s64 b7, %2, %7;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(kHalfB), "n"(kHalfB + 2), "n"(kHalfB + 4), "n"(kHalfB + 6)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Four of them, D (+)= A B with A in tensor memory (8 columns a step), B
+// MN-major; kStep: 16-byte units between B's 16-row steps
+template <uint32_t kStep>
+__device__ __forceinline__ void warp_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred e, p, t;\n\t"
+        ".reg .b32 a1, a2, a3;\n\t"
+        ".reg .b64 b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep)
+        : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
@@ -403,15 +513,6 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
 
 // ---- the attention ---------------------------------------------------------------------
 
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 template <bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -445,10 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(B(kBarQFull + i), 1);
             mbar_init(B(kBarQEmpty + i), 1);
-            mbar_init(B(kBarSFull + i), 1);
-            mbar_init(B(kBarPFull + i), 4);
             mbar_init(B(kBarPvDone + i), 1);
             mbar_init(B(kBarOFull + i), 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(B(kBarSFull + 2 * i + x), 1);
+                mbar_init(B(kBarPFull + 2 * i + x), 4);
+            }
             mbar_init(B(kBarOEmpty + i), 4);
             mbar_init(B(kBarStatFull + i), 4);
             mbar_init(B(kBarStatEmpty + i), 4);
@@ -470,16 +573,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     const bool dead = *abort != 0;
 
-    auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait(b, parity, abort, err); };
+    auto wait = [&](uint32_t b, uint32_t parity) { return wait_phase(b, parity, abort, err); };
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        regs_inc<192>();
         const int s = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + s * 128u;
         const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kOCol + s * 128u;
         const int tok_r = r / G;
-        uint32_t n_s = 0;                       // S tiles of this slot so far
+        uint32_t n_f[2] = {0, 0};               // phases seen of the two S buffers
+        uint32_t n_pv = 0, n_o = 0;             // products and items with tiles before this item
         bool ok = !dead;
         for (uint32_t it = 0; ok; ++it) {
             const uint32_t wi = it % kWork;
@@ -494,43 +597,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int free_to = min(w.e.pos0 + first, w.kv_len - 1);   // every row of the slot sees keys up to here
             const bool busy = __any_sync(0xFFFFFFFFu, valid);
             float m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < c; ++i, ++n_s) {
-                const int j = dual ? t0 + s + 2 * i : t0 + i;
-                ok = __all_sync(0xFFFFFFFFu, wait(B(kBarSFull + s), n_s & 1));
+            for (int u = 0; u < 2 * c; ++u) {
+                // half x of the slot's tile i: 64 keys, its own S and P
+                const int i = u >> 1, x = u & 1, j = dual ? t0 + s + 2 * i : t0 + i;
+                const uint32_t tX = tS + 64u * x;
+                ok = __all_sync(0xFFFFFFFFu, wait(B(kBarSFull + 2 * s + x), n_f[x]++ & 1));
                 if (!ok) break;
                 if (!busy) {                    // no row of this warp is in the item: P may be anything
-                    if (lane == 0) mbar_arrive(B(kBarPFull + s));
+                    if (lane == 0) mbar_arrive(B(kBarPFull + 2 * s + x));
                     continue;
                 }
                 tc_fence_after();
-                uint32_t sr[128];
+                uint32_t sr[64];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) tmem_ld32(tS + 32u * h, *reinterpret_cast<uint32_t (*)[32]>(&sr[32 * h]));
+                for (int q = 0; q < 2; ++q) tmem_ld32(tX + 32u * q, *reinterpret_cast<uint32_t (*)[32]>(&sr[32 * q]));
                 tmem_ld_wait();
                 float *sf = reinterpret_cast<float *>(sr);
-                if (j * kKeys + kKeys - 1 > free_to) {
-                    const int last = lim - j * kKeys;
+                const int key0 = j * kKeys + 64 * x;
+                if (key0 + 63 > free_to) {
+                    const int last = lim - key0;
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
+                    for (int k = 0; k < 64; ++k)
                         if (k > last) sf[k] = -INFINITY;
                 }
                 float mp[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mp[e] = fmaxf(sf[e], sf[8 + e]);
+                for (int e = 0; e < 8; ++e) mp[e] = fmax3_nan(sf[e], sf[8 + e], sf[16 + e]);
 #pragma unroll
-                for (int k = 16; k < 128; k += 16)
+                for (int k = 24; k < 56; k += 16)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mp[e] = fmax3(mp[e], sf[k + e], sf[k + 8 + e]);
-                const float mx =
-                    fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], fmax3(mp[5], mp[6], mp[7]))) * kScaleLog2;
-                // the maximum is raised only for a growth beyond 2^8 (weights
-                // stay below 2^8, the sum is taken to the same base)
-                const bool need = valid && mx > m + kRescaleThreshold;
-                if (__any_sync(0xFFFFFFFFu, need)) {
-                    const float mn = need ? mx : m;
-                    const float f = need ? exp2f(m - mn) : 1.0f;
-                    if (i > 0) {
-                        ok = __all_sync(0xFFFFFFFFu, wait(B(kBarPvDone + s), (n_s - 1) & 1));
+                    for (int e = 0; e < 8; ++e) mp[e] = fmax3_nan(mp[e], sf[k + e], sf[k + 8 + e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mp[e] = fmax3_nan(mp[e], mp[e + 4], sf[56 + e]);
+                const float mx = fmax3_nan(fmax3_nan(mp[0], mp[1], mp[2]), fmax3_nan(mp[3], sf[60], sf[61]),
+                                           fmax3_nan(sf[62], sf[63], sf[63])) *
+                                 kScaleLog2;
+                // The base is raised for a growth beyond 2^8 only (weights stay
+                // below 2^8, o and the sum share the base); a NaN or infinite
+                // score makes the row NaN, as its softmax is.
+                const bool need = valid && mx > m + kRescaleThreshold && mx < INFINITY;
+                if (__any_sync(0xFFFFFFFFu, valid && !(mx <= m + kRescaleThreshold))) {
+                    if (valid && !(mx < INFINITY)) l = __int_as_float(0x7FFFFFFF);
+                    const float f = need ? exp2f(m - mx) : 1.0f;
+                    if (u > 0) {
+                        // the product of the half before is complete (S of this
+                        // half came behind the one before that)
+                        ok = __all_sync(0xFFFFFFFFu, wait(B(kBarPvDone + s), (n_pv + u - 1) & 1));
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
@@ -544,39 +656,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     l *= f;
-                    m = mn;
+                    if (need) m = mx;
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;     // no key seen yet: every weight is 2^-inf = 0
-                const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), nm2 = pack2(nm, nm);
                 uint64_t lp[2] = {0, 0};
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float x0, x1;
-                        unpack2(ffma2(pack2(sf[32 * h + 2 * k], sf[32 * h + 2 * k + 1]), sc2, nm2), x0, x1);
-                        x0 = ex2_approx(x0);
-                        x1 = ex2_approx(x1);
-                        lp[k & 1] = fadd2(lp[k & 1], pack2(x0, x1));
-                        const __nv_bfloat162 pb = __floats2bfloat162_rn(x0, x1);
-                        pk[k] = *reinterpret_cast<const uint32_t *>(&pb);
-                    }
-                    tmem_st16(tS + 16u * h, pk);
-                }
+                uint32_t pk[16];
+                weights32(sf, nm, pk, lp);
+                tmem_st16(tX, pk);
+                weights32(sf + 32, nm, pk, lp);
+                tmem_st16(tX + 16u, pk);
                 float a0, a1;
                 unpack2(fadd2(lp[0], lp[1]), a0, a1);
                 l += a0 + a1;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(B(kBarPFull + s));
+                if (lane == 0) mbar_arrive(B(kBarPFull + 2 * s + x));
+            }
+            if (!ok) break;
+            n_pv += 2 * c;
+            if (c) {
+                ok = __all_sync(0xFFFFFFFFu, wait(B(kBarOFull + s), n_o++ & 1));
+                if (!ok) break;
+                tc_fence_after();
             }
             if (!ok) break;
             ok = __all_sync(0xFFFFFFFFu, it == 0 || wait(B(kBarStatEmpty + s), (it - 1) & 1));
             if (!ok) break;
             stat[s * 256 + r] = m;
             stat[s * 256 + 128 + r] = l;
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(B(kBarStatFull + s));
@@ -585,13 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ epilogue
-        regs_dec<80>();
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kOCol;
         if (!kPaged && p.a.slots && !dead)
             append_rows(p.a, static_cast<int64_t>(blockIdx.x) * 4 + quarter, static_cast<int64_t>(gridDim.x) * 4, lane);
         float amax = 0.0f;
-        uint32_t n_o[2] = {0, 0};               // items with tiles in each slot
         bool ok = !dead;
         for (uint32_t it = 0; ok; ++it) {
             const uint32_t wi = it % kWork;
@@ -604,7 +711,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (both && s == 1) break;
                 for (int q = s; q < (both ? 2 : s + 1) && ok; ++q) {
                     ok = __all_sync(0xFFFFFFFFu, wait(B(kBarStatFull + q), it & 1));
-                    if (ok && w.c[q]) ok = __all_sync(0xFFFFFFFFu, wait(B(kBarOFull + q), n_o[q]++ & 1));
                 }
                 if (!ok) break;
                 tc_fence_after();
@@ -706,73 +812,107 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && u) atomicMax(reinterpret_cast<unsigned *>(p.a.o_amax), u);
         }
     } else {
-        regs_dec<48>();
         if (warp < 14) {
             // -------------------------------------------------------- MMA issue of one slot
-            if (lane == 0) {
-                const int s = warp - 12;
-                const uint32_t tS = tmem + s * 128u, tO = tmem + kOCol + s * 128u;
-                constexpr uint32_t idesc_s = idesc_bf16(128, 128, 0, 0);
-                constexpr uint32_t idesc_o = idesc_bf16(128, 128, 0, 1);   // V MN-major
-                const uint64_t qd = sdesc_sw128(s0 + kQOff + s * kTileBytes, 16, 1024);
-                uint32_t n_kv = 0;              // K / V pairs before this item
-                uint32_t n_s = 0, n_q = 0;      // tiles and items of this slot
-                uint32_t k_par = 0, v_par = 0;  // parity of each barrier's next phase
-                bool ok = !dead;
-                for (uint32_t it = 0; ok; ++it) {
-                    const uint32_t wi = it % kWork;
-                    ok = wait(B(kBarWorkFull + wi), (it / kWork) & 1);
-                    if (!ok || items[wi].last) break;
-                    const Item &w = items[wi];
-                    const int n = w.t1 - w.t0, c = w.c[s], other = w.c[s ^ 1], dual = w.dual;
-                    mbar_arrive(B(kBarWorkEmpty + wi));
-                    if (c) {
-                        ok = wait(B(kBarQFull + s), n_q & 1);
-                        for (int i = 0; i < c && ok; ++i, ++n_s) {
-                            const int jj = dual ? s + 2 * i : i;
-                            const uint32_t ki = 2 * (n_kv + jj), vi = ki + 1;
-                            const uint32_t ks = ki % kRing, vs = vi % kRing;
-                            // a tile that only this slot reads is released by it alone
-                            const bool alone = dual || i >= other;
-                            const uint32_t set = alone ? (1 + s) * kRing : 0;
-                            ok = wait(B(kBarKFull + set + ks), (k_par >> (set + ks)) & 1);
-                            k_par ^= 1u << (set + ks);
-                            if (!ok) break;
-                            tc_fence_after();
-                            // S = Q K^T (P of the tile before was read by an
-                            // earlier product of this thread: in order)
-                            const uint64_t kd = sdesc_sw128(s0 + kRingOff + ks * kTileBytes, 16, L::kGroup);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_ss(tS, qd + (k >> 2) * 1024 + (k & 3) * 2, kd + (k >> 2) * (L::kHalf >> 4) + (k & 3) * 2,
-                                       idesc_s, k > 0);
-                            tc_commit(B(kBarSFull + s));
-                            tc_commit(B(kBarKvEmpty + ks));
-                            if (alone) tc_commit(B(kBarKvEmpty + ks));
-                            if (i == c - 1) tc_commit(B(kBarQEmpty + s));
-                            if (i == 0 && n_q > 0) ok = wait(B(kBarOEmpty + s), (n_q - 1) & 1);
-                            ok = ok && wait(B(kBarPFull + s), n_s & 1) &&
-                                 wait(B(kBarClean + set + vs), (v_par >> (set + vs)) & 1);
-                            v_par ^= 1u << (set + vs);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t vd = sdesc_sw128(s0 + kRingOff + vs * kTileBytes, L::kHalf, L::kGroup);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_ts(tO, tS + 8 * k, vd + k * (2 * L::kGroup >> 4), idesc_o, i > 0 || k > 0);
-                            tc_commit(B(kBarPvDone + s));
-                            tc_commit(B(kBarKvEmpty + vs));
-                            if (alone) tc_commit(B(kBarKvEmpty + vs));
-                            if (i == c - 1) tc_commit(B(kBarOFull + s));
+            const int s = warp - 12;
+            const uint32_t tS = tmem + s * 128u, tO = tmem + kOCol + s * 128u;
+            constexpr uint32_t idesc_s = idesc_bf16(128, 64, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16(128, 128, 0, 1);   // V MN-major
+            const uint64_t qd = sdesc_sw128(s0 + kQOff + s * kTileBytes, 16, 1024);
+            auto wwait = [&](uint32_t b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0; };
+            uint32_t stage = 0;             // of this item's first K tile
+            uint32_t n_s = 0, n_q = 0;      // tiles and items of this slot
+            uint32_t k_par = 0, v_par = 0;  // parity of each barrier's next phase
+            bool ok = !dead;
+            for (uint32_t it = 0; ok; ++it) {
+                const uint32_t wi = it % kWork;
+                ok = wwait(B(kBarWorkFull + wi), (it / kWork) & 1);
+                if (!ok || items[wi].last) break;
+                const int n = items[wi].t1 - items[wi].t0, c = items[wi].c[s], other = items[wi].c[s ^ 1];
+                const int dual = items[wi].dual;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B(kBarWorkEmpty + wi));
+                if (c) {
+                    ok = wwait(B(kBarQFull + s), n_q & 1);
+                    // this slot's first K stage; its next one is 2 (4: dual) stages on
+                    uint32_t ks = (stage + (dual && s ? 2 : 0)) % kRing;
+                    // a tile that only this slot reads is released by it alone
+                    auto alone = [&](int i) { return dual || i >= other; };
+                    auto set_of = [&](int i) { return alone(i) ? static_cast<uint32_t>((1 + s) * kRing) : 0u; };
+                    // S = Q K^T of half x of the K tile (P of this buffer was read
+                    // by an earlier product of this thread: in order)
+                    auto issue_s = [&](int x) {
+                        const uint64_t kd = sdesc_sw128(s0 + kRingOff + ks * kTileBytes + x * 8 * L::kGroup, 16, L::kGroup);
+                        warp_mma8_ss<(L::kHalf >> 4)>(tS + 64 * x, qd, kd, idesc_s);
+                        warp_commit(B(kBarSFull + 2 * s + x));
+                    };
+                    auto k_done = [&](int i) {      // behind the second half of S of tile i
+                        warp_commit(B(kBarKvEmpty + ks));
+                        if (alone(i)) warp_commit(B(kBarKvEmpty + ks));
+                        if (i == c - 1) warp_commit(B(kBarQEmpty + s));
+                    };
+                    uint32_t kb = set_of(0) + ks;
+                    ok = ok && wwait(B(kBarKFull + kb), (k_par >> kb) & 1);
+                    if (!ok) break;
+                    k_par ^= 1u << kb;
+                    tc_fence_after();
+                    issue_s(0);
+                    issue_s(1);
+                    k_done(0);
+                    for (int i = 0; i < c && ok; ++i, ++n_s) {
+                        const uint32_t vs = ks + 1 == kRing ? 0 : ks + 1;
+                        const uint32_t vb = set_of(i) + vs;
+                        ok = wwait(B(kBarClean + vb), (v_par >> vb) & 1);
+                        v_par ^= 1u << vb;
+                        if (i == 0 && n_q > 0) ok = ok && wwait(B(kBarOEmpty + s), (n_q - 1) & 1);
+                        constexpr uint32_t kStep = 2 * L::kGroup >> 4;
+                        const uint64_t vd = sdesc_sw128(s0 + kRingOff + vs * kTileBytes, L::kHalf, L::kGroup);
+                        ks += dual ? 4 : 2;
+                        if (ks >= kRing) ks -= kRing;
+                        const bool more = i + 1 < c;
+                        kb = set_of(i + 1) + ks;
+                        // Per half: P V, then S of the next tile's half over it.
+                        // Where the next K tile is still on its way (a long cache
+                        // streams at the memory's rate) both P V go first, so that
+                        // the V tile makes room for the next load.
+                        const uint32_t kpar = (k_par >> kb) & 1;
+                        auto k_here = [&]() { return __all_sync(0xFFFFFFFFu, mbar_test_wait(B(kBarKFull + kb), kpar)) != 0; };
+                        bool early = more && k_here();
+                        ok = ok && wwait(B(kBarPFull + 2 * s), n_s & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        warp_mma4_ts<kStep>(tO, tS, vd, idesc_o, i > 0);
+                        warp_commit(B(kBarPvDone + s));
+                        if (more && !early) early = k_here();
+                        if (early) issue_s(0);
+                        ok = wwait(B(kBarPFull + 2 * s + 1), n_s & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        warp_mma4_ts<kStep>(tO, tS + 64, vd + 4 * kStep, idesc_o, 1);
+                        warp_commit(B(kBarPvDone + s));
+                        warp_commit(B(kBarKvEmpty + vs));
+                        if (alone(i)) warp_commit(B(kBarKvEmpty + vs));
+                        if (!more) {
+                            warp_commit(B(kBarOFull + s));
+                        } else {
+                            if (!early) {
+                                ok = wwait(B(kBarKFull + kb), kpar);
+                                if (!ok) break;
+                                tc_fence_after();
+                                issue_s(0);
+                            }
+                            issue_s(1);
+                            k_done(i + 1);
                         }
-                        ++n_q;
+                        k_par ^= more ? 1u << kb : 0u;
                     }
-                    n_kv += n;
+                    ++n_q;
                 }
-                // every MMA issued completes before tensor memory is freed
-                tc_commit(B(kBarDrain + s));
-                mbar_wait_plain(B(kBarDrain + s), 0);
+                stage = (stage + 2u * static_cast<uint32_t>(n)) % kRing;
             }
+            // every MMA issued completes before tensor memory is freed
+            warp_commit(B(kBarDrain + s));
+            wait_drain(B(kBarDrain + s), 0);
             __syncwarp();
         } else if (warp == 14) {
             // -------------------------------------------------------- work list and loads
@@ -914,9 +1054,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) {
                 // loads in flight land before the CTA may exit
                 for (uint32_t i = 0; i < 4 * kRing; ++i)
-                    if (used >> i & 1) mbar_wait_plain(B(kBarKFull + i), par >> i & 1);
+                    if (used >> i & 1) wait_drain(B(kBarKFull + i), par >> i & 1);
                 for (int s = 0; s < 2; ++s)
-                    if (n_q[s]) mbar_wait_plain(B(kBarQFull + s), (n_q[s] - 1) & 1);
+                    if (n_q[s]) wait_drain(B(kBarQFull + s), (n_q[s] - 1) & 1);
             }
         } else {
             // -------------------------------------------------------- V tiles: clean and hand on
