@@ -112,10 +112,19 @@ struct alignas(16) Item {
 };
 static_assert(sizeof(Item) <= 64, "work ring entry");
 
+// A CTA's range of the paged work: its first item, and the item that begins in
+// the range and goes on past it (what the second kernel merges).
+struct alignas(16) Range {
+    Entry first;
+    int e, g, t0;        // entry, KV head and first tile of the first item
+    int end_e, end_g, end_t;     // where the range ends (before that tile)
+    Entry cut;
+    int cut_g, cut_to;   // its KV head and the CTA that ends it (0: no such item)
+};
+
 struct Header {          // start of the workspace
     int n_ent;
-    int counter;
-    int64_t tiles;       // K / V tiles of all entries (one head)
+    int counter;         // packed: next item
 };
 
 struct Params {
@@ -124,7 +133,9 @@ struct Params {
     int max_ent;
     Header *head;
     Entry *ent;
-    int64_t *prefix;     // [n_ent + 1] tiles before each entry (paged)
+    int64_t *prefix;     // [n_ent + 1] tiles before each entry (paged, work list kernel only)
+    Range *ranges;       // [grid] (paged)
+    int grid;            // CTAs of the attention
     float *part;         // [2 grid][part_rows](max, sum) then [part_rows][128]
     int part_rows;
     unsigned *err;
@@ -143,6 +154,16 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
     return d;
 }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -322,21 +343,14 @@ struct Layout {
 
 __device__ __forceinline__ int64_t range_begin(int64_t W, int c, int n) { return W * c / n; }
 
-// The entry that holds tile x of the head: the last e with prefix[e] <= x
-// (whole warp; 32 probes a step).
-__device__ __forceinline__ int find_entry(const int64_t *prefix, int n_ent, int64_t x, int lane) {
-    int lo = 0, hi = n_ent;                       // prefix[lo] <= x < prefix[hi]
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + lane * step;
-        const bool le = i < hi && prefix[i] <= x;
-        const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, le));   // lane 0 always holds
-        const int nlo = lo + k * step;
-        hi = min(hi, nlo + step);
-        lo = nlo;
-    }
-    return lo;
+// K / V tiles of an entry; cap: positions that a table row has pages for.
+__device__ __forceinline__ int entry_tiles(const Entry &e, int64_t cap) {
+    return static_cast<int>((min(static_cast<int64_t>(e.pos0) + e.ntok, cap) + kKeys - 1) / kKeys);
 }
+
+// Cost of one of its tiles: with queries in both slots twice that of a tile
+// that one slot takes while the other takes the next (measured 2.6 to 1.1 us).
+__device__ __forceinline__ int tile_cost(const Entry &e, int R) { return e.ntok > R ? 2 : 1; }
 
 // V of a new token i of the entry (for the rows that a cleaned value belongs to)
 template <bool kPaged>
@@ -461,23 +475,84 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
         r.ntok = min(tokens(lo) - first, TB);
         r.pos0 = ctx + first;
         r.kv = kPaged ? lo : start;
-        tiles = static_cast<int>((min(static_cast<int64_t>(r.pos0) + r.ntok, cap) + kKeys - 1) / kKeys);
+        tiles = entry_tiles(r, cap);
         return r;
     };
     if (kPaged) {
         int64_t at0 = 0;
         for (int e0 = 0; e0 < n_ent; e0 += kPrepThreads) {
             const int e = e0 + tid;
-            int tiles = 0;
-            if (e < n_ent) p.ent[e] = entry(e, tiles);
+            int tiles = 0, cost = 0;
+            if (e < n_ent) {
+                const Entry r = entry(e, tiles);
+                p.ent[e] = r;
+                cost = tiles * tile_cost(r, p.R);
+            }
             int64_t total;
-            const int64_t at = block_scan(tiles, red, &total);
+            const int64_t at = block_scan(cost, red, &total);
             if (e < n_ent) p.prefix[e] = at0 + at;
             at0 += total;
         }
-        if (tid == 0) {
-            p.prefix[n_ent] = at0;
-            p.head->tiles = at0;
+        if (tid == 0) p.prefix[n_ent] = at0;
+        __syncthreads();
+        // the ranges: equal shares of the cost of all entries and heads; a border
+        // inside an entry falls on its next whole tile
+        const int64_t W = at0 * a.Hkv;
+        // (a share holds one whole tile at least, so no range is empty)
+        const int64_t most = a.max_new > p.R ? max(W / 2, static_cast<int64_t>(1)) : W;
+        const int n = static_cast<int>(min(min(W, most), static_cast<int64_t>(p.grid)));
+        struct Place {
+            int e, g, t;                         // the tile that a border falls on
+        };
+        auto locate = [&](int c) {
+            const int64_t w = range_begin(W, c, n);
+            Place r;
+            r.g = static_cast<int>(w / at0);
+            const int64_t y = w - r.g * at0;
+            int lo = 0, hi = n_ent;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.prefix[mid] <= y) lo = mid; else hi = mid;
+            }
+            r.e = lo;
+            const Entry en = p.ent[lo];
+            const int u = tile_cost(en, p.R);
+            r.t = static_cast<int>((y - p.prefix[lo] + u - 1) / u);
+            if (r.t >= entry_tiles(en, cap)) {   // the entry's end: the next one with tiles
+                r.t = 0;
+                do {
+                    if (++r.e == n_ent) {
+                        r.e = 0;
+                        ++r.g;
+                    }
+                } while (r.g < a.Hkv && p.prefix[r.e + 1] == p.prefix[r.e]);
+            }
+            return r;
+        };
+        for (int c = tid; c < p.grid; c += kPrepThreads) {
+            Range r = {};
+            if (c < n) {
+                const Place lo = locate(c), hi = c + 1 < n ? locate(c + 1) : Place{0, a.Hkv, 0};
+                r.e = lo.e;
+                r.g = lo.g;
+                r.t0 = lo.t;
+                if (lo.g < a.Hkv) r.first = p.ent[lo.e];
+                r.end_e = hi.e;
+                r.end_g = hi.g;
+                r.end_t = hi.t;
+                // an item cut by the far border that begins in this range
+                if (hi.t > 0 && (hi.g != lo.g || hi.e != lo.e || lo.t == 0)) {
+                    r.cut = p.ent[hi.e];
+                    r.cut_g = hi.g;
+                    // the first border past its last tile's start, less one
+                    const int u = tile_cost(r.cut, p.R);
+                    const int64_t x = hi.g * at0 + p.prefix[hi.e] + static_cast<int64_t>(entry_tiles(r.cut, cap) - 1) * u + 1;
+                    r.cut_to = static_cast<int>(min((x * n + W - 1) / W, static_cast<int64_t>(n))) - 1;
+                }
+            } else {
+                r.g = r.end_g = a.Hkv;
+            }
+            p.ranges[c] = r;
         }
     } else {
         // counting sort by tiles, most first (the order within a bin does not
@@ -698,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kOCol;
         if (!kPaged && p.a.slots && !dead)
             append_rows(p.a, static_cast<int64_t>(blockIdx.x) * 4 + quarter, static_cast<int64_t>(gridDim.x) * 4, lane);
-        float amax = 0.0f;
+        __nv_bfloat162 amax2 = __floats2bfloat162_rn(0.0f, 0.0f);
         bool ok = !dead;
         for (uint32_t it = 0; ok; ++it) {
             const uint32_t wi = it % kWork;
@@ -746,24 +821,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __nv_bfloat16 *orow = p.a.o + static_cast<int64_t>(w.e.row0 + tok) * p.a.ldo + (w.g * G + r % G) * kD;
                 const int bad = w.bad;
+                const bool any = __any_sync(0xFFFFFFFFu, valid);
+                const uint64_t scale0 = pack2(f0 * inv, f0 * inv), scale1 = pack2(f1 * inv, f1 * inv);
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t ov[16];
-                    float f[16];
-                    if (one) {
-                        tmem_ld16(tO + s * 128u + 16u * c, ov);
-                        tmem_ld_wait();
+                for (int c = 0; any && c < 8; ++c) {
+                    uint32_t o0[16], o1[16];
+                    if (one) tmem_ld16(tO + s * 128u + 16u * c, o0);
+                    if (two) tmem_ld16(tO + 128u + 16u * c, o1);
+                    tmem_ld_wait();
+                    uint64_t f[8];              // pairs of o, scaled
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(ov[e]) * f0;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = 0.0f;
-                    }
+                    for (int e = 0; e < 8; ++e) f[e] = one ? fmul2(pair_of(o0[2 * e], o0[2 * e + 1]), scale0) : 0;
                     if (two) {
-                        tmem_ld16(tO + 128u + 16u * c, ov);
-                        tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(ov[e]), f1, f[e]);
+                        for (int e = 0; e < 8; ++e) f[e] = ffma2(pair_of(o1[2 * e], o1[2 * e + 1]), scale1, f[e]);
                     }
                     if (bad && valid) {
                         // cleaned values of the keys this row does see
@@ -771,23 +842,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const __nv_bfloat16 *v = new_value_row<kPaged>(p, w, k);
                             if (!v) continue;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float x = __bfloat162float(v[16 * c + e]);
-                                if (!isfinite(x)) f[e] += x;
+                            for (int e = 0; e < 8; ++e) {
+                                const float y0 = __bfloat162float(v[16 * c + 2 * e]), y1 = __bfloat162float(v[16 * c + 2 * e + 1]);
+                                f[e] = fadd2(f[e], pack2(isfinite(y0) ? 0.0f : y0, isfinite(y1) ? 0.0f : y1));
                             }
                         }
                     }
                     if (valid && w.part >= 0) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<float4 *>(po + 16 * c)[e] =
-                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            reinterpret_cast<ulonglong2 *>(po + 16 * c)[e] = make_ulonglong2(f[2 * e], f[2 * e + 1]);
                     } else if (valid) {
                         uint32_t pk[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e] * inv, f[2 * e + 1] * inv);
-                            amax = fmaxf(amax, fmaxf(fabsf(__bfloat162float(b.x)), fabsf(__bfloat162float(b.y))));
+                            float y0, y1;
+                            unpack2(f[e], y0, y1);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+                            if (p.a.o_amax) amax2 = __hmax2(amax2, __habs2(b));
                             pk[e] = *reinterpret_cast<const uint32_t *>(&b);
                         }
                         reinterpret_cast<uint4 *>(orow + 16 * c)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
@@ -808,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(B(kBarWorkEmpty + wi));
         }
         if (p.a.o_amax) {
+            const float amax = fmaxf(__bfloat162float(amax2.x), __bfloat162float(amax2.y));
             const unsigned u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
             if (lane == 0 && u) atomicMax(reinterpret_cast<unsigned *>(p.a.o_amax), u);
         }
@@ -918,17 +991,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- work list and loads
             const PagedAttnArgs &a = p.a;
             const int n_ent = p.head->n_ent;
-            const int64_t tiles = kPaged ? p.head->tiles : 0;
-            const int64_t W = tiles * a.Hkv;
-            const int grid = static_cast<int>(kPaged ? (W < gridDim.x ? W : gridDim.x) : gridDim.x);
-            int64_t at = 0, end = 0;
-            int g = 0, e = 0;
-            if (tiles > 0 && static_cast<int>(blockIdx.x) < grid) {
-                at = range_begin(W, blockIdx.x, grid);
-                end = range_begin(W, blockIdx.x + 1, grid);
-                g = static_cast<int>(at / max(tiles, static_cast<int64_t>(1)));
-                e = find_entry(p.prefix, n_ent, at - g * tiles, lane);
-            }
+            Range range = {};
+            if (kPaged) range = p.ranges[blockIdx.x];
+            int e = range.e, g = range.g;
             const int64_t cap = kPaged ? static_cast<int64_t>(a.max_pages) << a.ps_shift : INT32_MAX;
             const int page_rows = min(1 << a.ps_shift, kKeys);
             const int n_groups = page_rows / 8;                        // 8-row groups of a box
@@ -944,25 +1009,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item w = {};
                 w.last = 1;
                 if (kPaged) {
-                    if (at < end) {
-                        // (entries without tiles are passed over)
-                        int64_t pe;
-                        while ((pe = p.prefix[e + 1]) <= at - g * tiles) {
-                            if (++e == n_ent) {
-                                e = 0;
-                                ++g;
-                            }
+                    // (entries without tiles are passed over)
+                    int full = 0;
+                    const int from = it == 0 ? range.t0 : 0;
+                    while (g < range.end_g || (g == range.end_g && e < range.end_e) ||
+                           (g == range.end_g && e == range.end_e && from < range.end_t)) {
+                        w.e = it == 0 && e == range.e && g == range.g ? range.first : p.ent[e];
+                        full = entry_tiles(w.e, cap);
+                        if (full > 0) break;
+                        if (++e == n_ent) {
+                            e = 0;
+                            ++g;
                         }
-                        const int64_t pb = p.prefix[e], x = at - g * tiles;
-                        w.e = p.ent[e];
+                    }
+                    if (full > 0) {
                         w.g = g;
                         w.last = 0;
-                        w.t0 = static_cast<int>(x - pb);
-                        const int64_t stop = min(pe - pb, w.t0 + (end - at));
-                        w.t1 = static_cast<int>(stop);
+                        w.t0 = from;
+                        w.t1 = g == range.end_g && e == range.end_e ? range.end_t : full;
                         const int place = 2 * static_cast<int>(blockIdx.x);
-                        w.part = w.t0 > 0 ? place : (stop < pe - pb ? place + 1 : -1);
-                        at += w.t1 - w.t0;
+                        w.part = w.t0 > 0 ? place : (w.t1 < full ? place + 1 : -1);
+                        if (++e == n_ent) {
+                            e = 0;
+                            ++g;
+                        }
                     }
                 } else {
                     int idx = 0;
@@ -1132,48 +1202,57 @@ __global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const 
     const PagedAttnArgs &a = p.a;
     griddep_wait();
     griddep_launch_dependents();
-    const int n_ent = p.head->n_ent;
-    const int64_t tiles = p.head->tiles, W = tiles * a.Hkv;
-    const int grid = static_cast<int>(W < gridDim.x ? W : gridDim.x);
     const int c = blockIdx.x;
-    if (c >= grid - 1) return;
-    const int64_t lo = range_begin(W, c, grid), hi = range_begin(W, c + 1, grid);
-    const int g = static_cast<int>((hi - 1) / tiles);
-    const int e = find_entry(p.prefix, n_ent, hi - 1 - g * tiles, lane);
-    const int64_t is = g * tiles + p.prefix[e], ie = g * tiles + p.prefix[e + 1];
-    if (is < lo || ie <= hi) return;
-    int last = c + 1;
-    while (range_begin(W, last + 1, grid) < ie) ++last;
-    const Entry en = p.ent[e];
+    const Range rg = p.ranges[c];
+    if (rg.cut_to == 0) return;
+    const Entry en = rg.cut;
+    const int g = rg.cut_g, n = rg.cut_to - c + 1;
     const bool dual = en.ntok <= p.R;
     const int64_t stride = static_cast<int64_t>(p.part_rows) * (2 + kD);
+    // part k: c's second place, then the first places of the CTAs after it
+    const float *base0 = p.part + (2 * static_cast<int64_t>(c) + 1) * stride;
+    auto part = [&](int k) { return k == 0 ? base0 : base0 + (2 * k - 1) * stride; };
     float amax = 0.0f;
     const int rows = en.ntok * p.G;           // (token, head) pairs in order
     for (int i = blockIdx.y * kCombineRows + warp; i < rows; i += gridDim.y * kCombineRows) {
         const int tok = i / p.G, hh = i % p.G;
         const int prow = dual || tok < p.R ? i : kRows + (tok - p.R) * p.G + hh;
-        const float *first = p.part + (2 * static_cast<int64_t>(c) + 1) * stride;
-        float m = -INFINITY;
-        for (int k = c + lane; k <= last; k += 32)
-            m = fmaxf(m, (k == c ? first : p.part + 2 * static_cast<int64_t>(k) * stride)[prow * 2]);
+        // lanes take the parts' (maximum, sum); the parts' weights are then
+        // handed round, and their rows are loaded eight at a time
+        float m = -INFINITY, l = 0.0f;
+        for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)[prow * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        float l = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = c; k <= last; ++k) {
-            const float *base = k == c ? first : p.part + 2 * static_cast<int64_t>(k) * stride;
-            const float2 ml = *reinterpret_cast<const float2 *>(base + prow * 2);
-            const float4 v = reinterpret_cast<const float4 *>(base + p.part_rows * 2 + static_cast<int64_t>(prow) * kD)[lane];
-            // (a part without a key for this row: maximum -inf, sum and o 0 or,
-            // where a value was not finite, that value)
-            const float f = ml.x > -INFINITY ? exp2f(ml.x - m) : 1.0f;
-            l = fmaf(ml.y, f, l);
-            acc.x = fmaf(v.x, f, acc.x);
-            acc.y = fmaf(v.y, f, acc.y);
-            acc.z = fmaf(v.z, f, acc.z);
-            acc.w = fmaf(v.w, f, acc.w);
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            float f = 0.0f;
+            if (k0 + lane < n) {
+                const float2 ml = *reinterpret_cast<const float2 *>(part(k0 + lane) + prow * 2);
+                // (a part without a key for this row: maximum -inf, sum and o 0
+                // or, where a value was not finite, that value)
+                f = ml.x > -INFINITY ? exp2f(ml.x - m) : 1.0f;
+                l = fmaf(ml.y, f, l);
+            }
+            const int kn = min(n - k0, 32);
+            for (int k = 0; k < kn; k += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = k + u < kn ? reinterpret_cast<const float4 *>(part(k0 + k + u) + p.part_rows * 2 +
+                                                                        static_cast<int64_t>(prow) * kD)[lane]
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k + u);
+                    acc.x = fmaf(v[u].x, fk, acc.x);
+                    acc.y = fmaf(v[u].y, fk, acc.y);
+                    acc.z = fmaf(v[u].z, fk, acc.z);
+                    acc.w = fmaf(v[u].w, fk, acc.w);
+                }
+            }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
         reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(en.row0 + tok) * a.ldo + (g * p.G + hh) * kD)[lane] =
@@ -1216,7 +1295,7 @@ bool encode(CUtensorMap *m, int rank, const void *base, const cuuint64_t *dims, 
 }
 
 struct Workspace {
-    size_t ent, prefix, part, total;
+    size_t ent, prefix, ranges, part, total;
     int max_ent, part_rows;
 };
 
@@ -1227,7 +1306,8 @@ Workspace carve(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv, b
     w.max_ent = static_cast<int>(T / (2 * R) + B);
     w.ent = 256;
     w.prefix = up(w.ent + sizeof(Entry) * w.max_ent);
-    w.part = paged ? up(w.prefix + sizeof(int64_t) * (w.max_ent + 1)) : w.prefix;
+    w.ranges = paged ? up(w.prefix + sizeof(int64_t) * (w.max_ent + 1)) : w.prefix;
+    w.part = paged ? up(w.ranges + sizeof(Range) * num_sms) : w.ranges;
     // (an even count keeps the 16-byte alignment of the rows behind the (max, sum) pairs)
     w.part_rows = paged ? static_cast<int>(max_new <= R ? (max_new * G + 1) / 2 * 2 : 2 * kRows) : 0;
     w.total = up(w.part + sizeof(float) * 2 * num_sms * w.part_rows * (2 + kD));
@@ -1283,6 +1363,8 @@ cudaError_t launch_attention_paged(const PagedAttnArgs &a, void *ws, unsigned *e
     p.head = reinterpret_cast<Header *>(base);
     p.ent = reinterpret_cast<Entry *>(base + w.ent);
     p.prefix = reinterpret_cast<int64_t *>(base + w.prefix);
+    p.ranges = reinterpret_cast<Range *>(base + w.ranges);
+    p.grid = grid;
     p.part = reinterpret_cast<float *>(base + w.part);
     p.part_rows = w.part_rows;
     p.err = err;
