@@ -138,6 +138,7 @@ struct Params {
     int64_t *prefix;     // [n_ent + 1] tiles before each entry (paged, work list kernel only)
     Range *ranges;       // [grid] (paged)
     int grid;            // CTAs of the attention
+    int self;            // the CTAs find their work themselves (few sequences, see launch_kind)
     float *part;         // [2 grid][part_rows](max, sum) then [part_rows][128]
     int part_rows;
     unsigned *err;
@@ -183,17 +184,49 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// 2^x of a pair on the FMA and integer pipes: x = n + f with n the nearest
+// integer (read from the low bits of x + 1.5 2^23), 2^f by the cubic 1 + f (...)
+// of least relative error on [-0.5, 0.5] (1.0e-4, fitted here by Lawson
+// iteration; the result is rounded to BF16, 2e-3), n added to the exponent.
+// From -127 down (masked scores): exactly 0, as 2^0 is exactly 1.  x < 128.
+__device__ __forceinline__ void exp2_pair_fma(uint64_t x, float &y0, float &y1) {
+    float x0, x1;
+    unpack2(x, x0, x1);
+    x = pack2(fmaxf(x0, -127.0f), fmaxf(x1, -127.0f));
+    const uint64_t t = fadd2(x, pack2(12582912.0f, 12582912.0f));
+    const uint64_t n = fadd2(t, pack2(-12582912.0f, -12582912.0f));
+    const uint64_t f = ffma2(n, pack2(-1.0f, -1.0f), x);
+    uint64_t p = ffma2(f, pack2(0.05500893294811249f, 0.05500893294811249f), pack2(0.24221095442771912f, 0.24221095442771912f));
+    p = ffma2(p, f, pack2(0.6932829022407532f, 0.6932829022407532f));
+    p = ffma2(p, f, pack2(1.0f, 1.0f));
+    float t0, t1, p0, p1;
+    unpack2(t, t0, t1);
+    unpack2(p, p0, p1);
+    y0 = __uint_as_float((__float_as_uint(t0) << 23) + __float_as_uint(p0));
+    y1 = __uint_as_float((__float_as_uint(t1) << 23) + __float_as_uint(p1));
+}
+
 // Weights of 32 scores to the base 2^-nm as BF16 pairs, their sum (of the
-// unrounded weights) added to lp.
+// unrounded weights) added to lp.  Of each 16 pairs kExpFma take the FMA pipes:
+// the transcendental unit (16 a clock per SM) needs as long for a tile's
+// exponentials as the tensor cores for its products.  Measured with 0 / 3 / 4 /
+// 5 / 6 of 16: 16384 tokens over 49152 17.7 / 16.9 / 16.3 / 16.1 / 16.6 ms,
+// 8192-token prompt 581 / 571 / 562 / 557 / 570 us, ragged prompts 519 / 523 /
+// 527 / 529 / 535 us, 64 decode rows 129 / - / 131 / 134 / - us.
+constexpr int kExpFma = 4;
 __device__ __forceinline__ void weights32(const float *s, float nm, uint32_t (&pk)[16], uint64_t (&lp)[2]) {
     const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), nm2 = pack2(nm, nm);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const uint64_t x = ffma2(pack2(s[2 * k], s[2 * k + 1]), sc2, nm2);
         float y0, y1;
-        unpack2(x, y0, y1);
-        y0 = ex2_approx(y0);
-        y1 = ex2_approx(y1);
+        if ((k + 1) * kExpFma / 16 > k * kExpFma / 16) {
+            exp2_pair_fma(x, y0, y1);
+        } else {
+            unpack2(x, y0, y1);
+            y0 = ex2_approx(y0);
+            y1 = ex2_approx(y1);
+        }
         lp[k & 1] = fadd2(lp[k & 1], pack2(y0, y1));
         const __nv_bfloat162 pb = __floats2bfloat162_rn(y0, y1);
         pk[k] = *reinterpret_cast<const uint32_t *>(&pb);
@@ -351,8 +384,11 @@ __device__ __forceinline__ int entry_tiles(const Entry &e, int64_t cap) {
 }
 
 // Cost of one of its tiles: with queries in both slots twice that of a tile
-// that one slot takes while the other takes the next (measured 2.6 to 1.1 us).
-__device__ __forceinline__ int tile_cost(const Entry &e, int R) { return e.ntok > R ? 2 : 1; }
+// that one slot takes while the other takes the next (alone 2.6 and 1.1 us, but
+// among others the first is held up less; four chunks beside 60 single tokens:
+// 440 us at equal cost, 361 at 2 : 1, 386 at 7 : 4, 396 at 5 : 2).
+constexpr int kCostTwo = 2, kCostOne = 1;
+__device__ __forceinline__ int tile_cost(const Entry &e, int R) { return e.ntok > R ? kCostTwo : kCostOne; }
 
 // V of a new token i of the entry (for the rows that a cleaned value belongs to)
 template <bool kPaged>
@@ -501,8 +537,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
         // inside an entry falls on its next whole tile
         const int64_t W = at0 * a.Hkv;
         // (a share holds one whole tile at least, so no range is empty)
-        const int64_t most = a.max_new > p.R ? max(W / 2, static_cast<int64_t>(1)) : W;
-        const int n = static_cast<int>(min(min(W, most), static_cast<int64_t>(p.grid)));
+        const int64_t most = min(W, max(W / (a.max_new > p.R ? kCostTwo : kCostOne), static_cast<int64_t>(1)));
+        const int n = static_cast<int>(min(most, static_cast<int64_t>(p.grid)));
         struct Place {
             int e, g, t;                         // the tile that a border falls on
         };
@@ -589,6 +625,37 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
 }
 
 // ---- the attention ---------------------------------------------------------------------
+
+// The work of a packed call with at most 32 sequences and at most one item a
+// CTA, found by the loading warp of each CTA itself (a lane holds a sequence);
+// spares the list kernel.
+struct SelfPlan {
+    int row0, ntok, pre, size;       // size: blocks of 2 R tokens; pre: of the sequences before
+
+    // returns the blocks of all sequences
+    __device__ __forceinline__ int take(const Params &p, int lane) {
+        const PagedAttnArgs &a = p.a;
+        row0 = ntok = size = 0;
+        if (lane < a.B) {
+            row0 = min(max(a.cu[lane], 0), a.T);
+            ntok = max(min(max(a.cu[lane + 1], 0), a.T) - row0, 0);
+            size = (ntok + 2 * p.R - 1) / (2 * p.R);
+        }
+        int x = size;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        pre = x - size;
+        return __shfl_sync(0xFFFFFFFFu, x, 31);
+    }
+    __device__ __forceinline__ Entry block(int i, int tokens) const {
+        const int b = 31 - __clz(__ballot_sync(0xFFFFFFFFu, size > 0 && pre <= i) | 1u);
+        const int first = (i - __shfl_sync(0xFFFFFFFFu, pre, b)) * tokens, start = __shfl_sync(0xFFFFFFFFu, row0, b);
+        return Entry{start + first, min(__shfl_sync(0xFFFFFFFFu, ntok, b) - first, tokens), first, start};
+    }
+};
 
 template <bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -825,8 +892,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int bad = w.bad;
                 const bool any = __any_sync(0xFFFFFFFFu, valid);
                 const uint64_t scale0 = pack2(f0 * inv, f0 * inv), scale1 = pack2(f1 * inv, f1 * inv);
+                const bool plain = one && !two && !bad && w.part < 0;
+                if (any && plain) {
+                    // the usual case: the next 16 columns are on their way while
+                    // these are rounded and stored
+                    uint32_t ov[16];
+                    tmem_ld16(tO + s * 128u, ov);
 #pragma unroll 1
-                for (int c = 0; any && c < 8; ++c) {
+                    for (int c = 0; c < 8; ++c) {
+                        tmem_ld_wait();
+                        uint64_t f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = fmul2(pair_of(ov[2 * e], ov[2 * e + 1]), scale0);
+                        if (c < 7) tmem_ld16(tO + s * 128u + 16u * (c + 1), ov);
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float y0, y1;
+                            unpack2(f[e], y0, y1);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+                            pk[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        if (p.a.o_amax && valid) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                amax2 = __hmax2(amax2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[e])));
+                        }
+                        if (valid) {
+                            reinterpret_cast<uint4 *>(orow + 16 * c)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            reinterpret_cast<uint4 *>(orow + 16 * c)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                        }
+                        __syncwarp();
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; any && !plain && c < 8; ++c) {
                     uint32_t o0[16], o1[16];
                     if (one) tmem_ld16(tO + s * 128u + 16u * c, o0);
                     if (two) tmem_ld16(tO + 128u + 16u * c, o1);
@@ -992,11 +1092,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 14) {
             // -------------------------------------------------------- work list and loads
             const PagedAttnArgs &a = p.a;
-            const int n_ent = p.head->n_ent;
-            Range range = {};
-            if (kPaged) range = p.ranges[blockIdx.x];
-            int e = range.e, g = range.g;
             const int64_t cap = kPaged ? static_cast<int64_t>(a.max_pages) << a.ps_shift : INT32_MAX;
+            Range range = {};
+            int n_ent;
+            SelfPlan plan;
+            if (!kPaged && p.self) {
+                n_ent = plan.take(p, lane);
+            } else {
+                n_ent = p.head->n_ent;
+                if (kPaged) range = p.ranges[blockIdx.x];
+            }
+            int e = range.e, g = range.g;
             const int page_rows = min(1 << a.ps_shift, kKeys);
             const int n_groups = page_rows / 8;                        // 8-row groups of a box
             const int boxes = kPaged ? kKeys / page_rows : 1;          // boxes of a tile
@@ -1037,11 +1143,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else {
-                    int idx = 0;
-                    if (lane == 0) idx = atomicAdd(&p.head->counter, 1);
-                    idx = __shfl_sync(0xFFFFFFFFu, idx, 0);
+                    int idx = blockIdx.x;
+                    if (p.self) {                // one item a CTA
+                        if (it > 0) idx = INT32_MAX;
+                    } else {
+                        if (lane == 0) idx = atomicAdd(&p.head->counter, 1);
+                        idx = __shfl_sync(0xFFFFFFFFu, idx, 0);
+                    }
                     if (n_ent > 0 && idx < static_cast<int64_t>(n_ent) * a.Hkv) {
-                        w.e = p.ent[idx / a.Hkv];
+                        w.e = p.self ? plan.block(idx / a.Hkv, 2 * R) : p.ent[idx / a.Hkv];
                         w.g = idx % a.Hkv;
                         w.last = 0;
                         w.t1 = (w.e.pos0 + w.e.ntok + kKeys - 1) / kKeys;
@@ -1335,13 +1445,21 @@ static cudaError_t launch_kind(Params &p, const CUtensorMap &tq, const CUtensorM
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_attention_kernel<kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    int prep_grid = 1;
-    if (kPaged && a.slots) {
-        const int64_t warps = static_cast<int64_t>(a.T) * a.Hkv;      // at most four rows a warp's turn
-        prep_grid += static_cast<int>(std::min<int64_t>((warps + 4 * 32 - 1) / (4 * 32), 2 * grid));
+    // Few short prompts: no work list (three of 348 tokens in all: 16.3 against
+    // 19.3 us with it; paged calls gained nothing, their list kernel also writes
+    // the new cache rows).
+    p.self = !kPaged && a.B <= 32 && (a.T / (2 * p.R) + a.B) * static_cast<int64_t>(a.Hkv) <= grid;
+    if (p.self) {
+        if (a.o_amax && (e = cudaMemsetAsync(a.o_amax, 0, sizeof(float), s)) != cudaSuccess) return e;
+    } else {
+        int prep_grid = 1;
+        if (kPaged && a.slots) {
+            const int64_t warps = static_cast<int64_t>(a.T) * a.Hkv;      // at most four rows a warp's turn
+            prep_grid += static_cast<int>(std::min<int64_t>((warps + 4 * 32 - 1) / (4 * 32), 2 * grid));
+        }
+        e = launch_pdl(paged_prep_kernel<kPaged>, dim3(prep_grid), dim3(kPrepThreads), prep_smem, s, p);
+        if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(paged_prep_kernel<kPaged>, dim3(prep_grid), dim3(kPrepThreads), prep_smem, s, p);
-    if (e != cudaSuccess) return e;
     e = launch_pdl(paged_attention_kernel<kPaged>, dim3(grid), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (kPaged) {
