@@ -388,8 +388,9 @@ size_t mq_attention_packed_workspace_bytes(int64_t T, int64_t B, int64_t H, int6
  * values are also written to its slot; rows whose slot is outside the cache
  * are not.  No two rows may name one slot.  o_amax (device, one float, or
  * NULL) receives max |o| over the rows below cu_lens[B], ready for
- * mq_quantize_nvfp4 with n_partials = 1.  A non-finite key or value reaches
- * only rows that attend to it.  Requirements: D == 128, H % Hkv == 0,
+ * mq_quantize_nvfp4 with n_partials = 1 (NaN values are passed over).  A
+ * non-finite key or value reaches only rows that attend to it; a row whose
+ * every score is -inf is NaN.  Requirements: D == 128, H % Hkv == 0,
  * H / Hkv <= 128, H <= 1024; qkv, o, pages and workspace 16-byte aligned;
  * workspace (device) of at least mq_attention_packed_workspace_bytes bytes,
  * not shared with a call that may run at the same time.  Bounded waits: a

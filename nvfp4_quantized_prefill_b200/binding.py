@@ -15,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmq.so")
 
 MQ_AMAX_PARTIALS_MAX = 4096
+MQ_PAGED_MAX_REQUESTS, MQ_PAGED_MAX_TOKENS = 16384, 1 << 22
 STATUS = {0: "MQ_OK", 1: "MQ_ERR_INVALID_ARG", 2: "MQ_ERR_SHAPE", 3: "MQ_ERR_ALIGNMENT",
           4: "MQ_ERR_UNSUPPORTED_DEVICE", 5: "MQ_ERR_OOM", 6: "MQ_ERR_CUDA", 7: "MQ_ERR_TIMEOUT"}
 

@@ -876,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool two = both && w.c[1] > 0;
                 const bool one = w.c[s] > 0;
-                const float inv = w.part >= 0 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);   // no key: zeros
+                // (a row sees one key at least; sum 0: every score is -inf, and o is 0 x inf = NaN)
+                const float inv = w.part >= 0 ? 1.0f : 1.0f / l;
                 const int prow = (both ? 0 : s * kRows) + r;
                 float *pm = nullptr, *po = nullptr;
                 if (w.part >= 0) {
@@ -1365,7 +1366,7 @@ __global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const 
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = 1.0f / l;
         __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
         reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(en.row0 + tok) * a.ldo + (g * p.G + hh) * kD)[lane] =
             *reinterpret_cast<uint2 *>(r);

@@ -367,6 +367,49 @@ def test_nonfinite_rows_reach_only_rows_that_attend_to_them(value, paged):
         assert mq.mq_check() == 0
 
 
+@pytest.mark.parametrize("ctx,new,paged", [(0, 150, False), (0, 1, False), (37, 30, True), (900, 1, True), (300, 200, True)])
+def test_rows_whose_every_score_is_minus_infinity_are_nan(ctx, new, paged):
+    """Their softmax is 0 / 0, as in the formula; the sequence beside them is
+    not touched."""
+    H, Hkv = 8, 2
+    st = Step([ctx, 20 if paged else 0], [new, 40], H, Hkv, 16, seed=31)
+    heads = torch.arange(H) * D
+    for s in st.seqs[:1]:
+        s[:, heads] = 1.0
+        s[:, H * D + torch.arange(Hkv) * D] = float("-inf")
+    st.qkv[:new, : st.ldqkv] = st.seqs[0][ctx:].cuda()
+    st._put(st.k, st.v, 0, 0, ctx)
+    (st.paged if paged else st.packed)()
+    torch.cuda.synchronize()
+    assert torch.isnan(st.o[:new]).all()
+    q, k, v = _split(st.seqs[1], H, Hkv)
+    c = st.ctx[1]
+    ref, a = oracle.attention(q[c:], k, v, H, Hkv, D, pos0=c)
+    assert_close(st.o[new:st.n], ref, a, "the other sequence")
+    assert mq.mq_check() == 0
+
+
+@pytest.mark.parametrize("gone,ctx,new", [(200, 700, 1), (200, 300, 60), (129, 0, 300), (640, 3000, 5)])
+def test_keys_with_a_score_of_minus_infinity_have_no_weight(gone, ctx, new):
+    """The first keys of a sequence are -inf: rows behind them attend to the
+    others as if those were not there."""
+    H, Hkv = 8, 2
+    st = Step([ctx], [new], H, Hkv, 16, seed=32)
+    s = st.seqs[0]
+    s[:, torch.arange(H) * D] = 1.0
+    s[:gone, H * D + torch.arange(Hkv) * D] = float("-inf")
+    st.qkv[:new, : st.ldqkv] = s[ctx:].cuda()
+    st._put(st.k, st.v, 0, 0, ctx)
+    st.paged()
+    torch.cuda.synchronize()
+    q, k, v = _split(s, H, Hkv)
+    first = max(ctx, gone)
+    ref, a = oracle.attention(q[first:], k[gone:], v[gone:], H, Hkv, D, pos0=first - gone)
+    assert_close(st.o[first - ctx:new], ref, a, "rows behind the keys")
+    assert torch.isnan(st.o[: first - ctx]).all()
+    assert mq.mq_check() == 0
+
+
 def test_bad_pages_and_slots_stay_inside_the_cache():
     """Slots outside the cache are skipped; a table entry outside it reads as
     zeros; nothing else of the pool changes and no other sequence's rows do."""
@@ -406,6 +449,87 @@ def test_a_table_row_that_is_too_short_drops_the_keys_past_it():
     assert mq.mq_check() == 0
 
 
+def test_rows_past_max_new_are_left_as_they_were():
+    """A sequence with more rows than max_new: the first max_new are computed,
+    the cache gets them all."""
+    H, Hkv, ps = 8, 2, 16
+    st = Step([50, 0, 300], [9, 60, 1], H, Hkv, ps, seed=14)
+    st.paged(max_new=5)
+    torch.cuda.synchronize()
+    amax = 0.0
+    for b, s in enumerate(st.seqs):
+        q, k, v = _split(s, H, Hkv)
+        c, n = st.ctx[b], min(st.new[b], 5)
+        ref, a = oracle.attention(q[c:c + n], k[:c + n], v[:c + n], H, Hkv, D, pos0=c)
+        got = st.o[st.cu[b]:st.cu[b + 1]]
+        assert_close(got[:n], ref, a, f"sequence {b}")
+        assert (got[n:] == 3.0).all()
+        amax = max(amax, float(got[:n].float().abs().max()))
+    assert float(st.amax) == amax
+    kr, vr = st.k0.cpu(), st.v0.cpu()
+    for b in range(3):
+        st._put(kr, vr, b, st.ctx[b], st.ctx[b] + st.new[b])
+    assert torch.equal(st.k.cpu().view(torch.int16), kr.view(torch.int16))
+    assert torch.equal(st.v.cpu().view(torch.int16), vr.view(torch.int16))
+    assert mq.mq_check() == 0
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_as_many_requests_as_there_may_be(paged):
+    """One token each without context attends to itself alone (weight 1), so o
+    is its value, bit for bit, in every head of the group."""
+    B, H, Hkv, ps = mq.MQ_PAGED_MAX_REQUESTS, 4, 2, 8
+    qkv = _qkv(B, H, Hkv, 41).cuda()
+    cols = qkv.shape[1]
+    slots = torch.randperm(B, generator=torch.Generator().manual_seed(1)).cuda() * ps
+    k = torch.full((B, Hkv, ps, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    o = torch.full((B, H * D), 3.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    if paged:
+        table, ctx = (slots // ps).to(torch.int32).view(B, 1).contiguous(), torch.zeros(B, dtype=torch.int32, device="cuda")
+        nb = mq.mq_attention_paged_workspace_bytes(B, B, 1, H, Hkv, D)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        mq.mq_attention_paged_bf16(qkv, cols, B, cu, ctx, B, 1, H, Hkv, D, slots, table, 1, k, v, B, ps, o, H * D, None,
+                                   ws, nb)
+    else:
+        nb = mq.mq_attention_packed_workspace_bytes(B, B, H, Hkv, D)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        mq.mq_attention_packed_bf16(qkv, cols, B, cu, B, H, Hkv, D, slots, k, v, B, ps, o, H * D, None, ws, nb)
+    torch.cuda.synchronize()
+    _, kn, vn = _split(qkv, H, Hkv)
+    want = vn.view(B, Hkv, 1, D).expand(B, Hkv, H // Hkv, D).reshape(B, H * D)
+    assert torch.equal(o, want)
+    pages = slots // ps
+    assert torch.equal(k[pages, :, 0].reshape(B, -1), kn) and torch.equal(v[pages, :, 0].reshape(B, -1), vn)
+    assert torch.isnan(k[:, :, 1:]).all() and torch.isnan(v[:, :, 1:]).all()
+    assert mq.mq_check() == 0
+
+
+def test_a_cache_whose_offsets_pass_32_bits():
+    """Pages beyond 2^32 bytes (and 2^31 elements) into each array."""
+    H, Hkv, ps = 8, 2, 64
+    n_pages = (1 << 33) // (Hkv * ps * D * 2) + 16                 # 8 GiB and a little
+    st = Step([0, 200, 1000], [70, 1, 5], H, Hkv, ps, seed=15)
+    high = torch.zeros(n_pages, Hkv, ps, D, dtype=torch.bfloat16, device="cuda")
+    highv = torch.zeros_like(high)
+    n0 = st.n_pages
+    move = lambda p: n_pages - 1 - p if p % 2 else n_pages // 2 + p      # noqa: E731 (half of them past 4 GiB only)
+    ids = torch.tensor([move(p) for p in range(n0)], device="cuda")
+    high[ids], highv[ids] = st.k, st.v
+    small = st.k, st.v
+    st.table = [[move(p) if p >= 0 else p for p in r] for r in st.table]
+    st.slots_d = ids[(st.slots_d // ps)] * ps + st.slots_d % ps
+    st.k, st.v, st.n_pages = high, highv, n_pages
+    st.paged()
+    torch.cuda.synchronize()
+    st.k, st.v = high[ids], highv[ids]
+    inv = {move(p): p for p in range(n0)}
+    st.table = [[inv.get(p, p) for p in r] for r in st.table]
+    st.check("high pages")
+    del small
+
+
 # -- streams, graphs, and the loop -----------------------------------------------------------
 
 def test_another_stream_and_repeated_calls_give_the_same_bits():
@@ -421,6 +545,69 @@ def test_another_stream_and_repeated_calls_give_the_same_bits():
         outs.append((a.o, b.o))
     for x, y in outs[1:]:
         assert torch.equal(x, outs[0][0]) and torch.equal(y, outs[0][1])
+    assert mq.mq_check() == 0
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with workspaces of their own, over and over: the
+    same bits as one after the other."""
+    mk = lambda: (Step([0] * 5, [900, 77, 300, 1, 500], 16, 4, 16, seed=23),       # noqa: E731
+                  Step([3000, 90, 2000, 64], [40, 1, 1, 300], 16, 4, 16, seed=24))
+    a0, b0 = mk()
+    a0.packed()
+    b0.paged()
+    a1, b1 = mk()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # (arguments first, so that the calls follow one another closely)
+    a1.packed(sa)
+    b1.paged(stream=sb)
+    torch.cuda.synchronize()
+    B, H, Hkv = 5, 16, 4
+    for _ in range(20):
+        a1.o.fill_(3.0)
+        b1.o.fill_(3.0)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            mq.mq_attention_packed_bf16(a1.qkv, a1.ldqkv, a1.T, a1.cu_d, B, H, Hkv, D, a1.slots_d, a1.k, a1.v, a1.n_pages,
+                                        a1.ps, a1.o, a1.o.stride(0), a1.amax, a1.ws, a1.ws.numel(), sa)
+            mq.mq_attention_paged_bf16(b1.qkv, b1.ldqkv, b1.T, b1.cu_d, b1.ctx_d, 4, 300, H, Hkv, D, b1.slots_d, b1.table_d,
+                                       b1.max_pages, b1.k, b1.v, b1.n_pages, b1.ps, b1.o, b1.o.stride(0), b1.amax, b1.ws,
+                                       b1.ws.numel(), sb)
+        torch.cuda.synchronize()
+        assert torch.equal(a1.o, a0.o) and torch.equal(b1.o, b0.o)
+        assert float(a1.amax) == float(a0.amax) and float(b1.amax) == float(b0.amax)
+    assert mq.mq_check() == 0
+
+
+def test_captured_prompts_are_replayed_with_other_lengths():
+    """A packed call by itself in a graph, max |o| included: prompts short
+    enough to need no work list of their own, then others."""
+    H, Hkv, T, B = 8, 2, 200, 3
+    lens = [[40, 100, 60], [200, 0, 0], [1, 1, 1], [0, 0, 150], [0, 0, 0]]
+    st = Step([0, 0, 0], lens[0], H, Hkv, 0, seed=25)
+    nb = mq.mq_attention_packed_workspace_bytes(T, B, H, Hkv, D)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    cu = _i32([0, 0, 0, 0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mq.mq_attention_packed_bf16(st.qkv, st.ldqkv, T, cu, B, H, Hkv, D, None, None, None, 0, 0, st.o, H * D, st.amax,
+                                    ws, nb)
+    rows = st.qkv.cpu()
+    for ls in lens:
+        cu.copy_(_i32([0] + np.cumsum(ls).tolist()))
+        st.o.fill_(3.0)
+        st.amax.fill_(99.0)
+        g.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for n in ls:
+            if n:
+                ref, a = oracle.attention(*_split(rows[at:at + n], H, Hkv), H, Hkv, D)
+                assert_close(st.o[at:at + n], ref, a, f"prompt of {n} in {ls}")
+            at += n
+        assert (st.o[at:] == 3.0).all()
+        assert float(st.amax) == (float(st.o[:at].float().abs().max()) if at else 0.0)
     assert mq.mq_check() == 0
 
 
