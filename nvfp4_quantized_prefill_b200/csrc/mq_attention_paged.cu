@@ -52,13 +52,13 @@ constexpr int kRows = 128;                          // rows of a slot's tile
 constexpr int kKeys = 128;                          // keys of a K / V tile
 constexpr uint32_t kTileBytes = 128 * kD * 2;       // 32 KB: a Q, K or V tile
 constexpr int kRing = 5;                            // K / V tiles in flight or in use
-constexpr int kWork = 2;                            // items known ahead
+constexpr int kWork = 4;                            // items known ahead
 constexpr uint32_t kQOff = 0;                       // a Q tile per slot
 constexpr uint32_t kRingOff = 2 * kTileBytes;
 constexpr uint32_t kStatOff = kRingOff + kRing * kTileBytes;     // [2 slots][max, sum][128] floats
 constexpr uint32_t kWorkOff = kStatOff + 2 * 2 * kRows * 4;      // [kWork] items
 constexpr uint32_t kBarOff = kWorkOff + kWork * 64;
-constexpr uint32_t kSmemBytes = kBarOff + 560;
+constexpr uint32_t kSmemBytes = kBarOff + 592;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;                 // S0, S1, O0, O1
@@ -84,7 +84,7 @@ enum : uint32_t {
     kBarClean = kBarKvEmpty + kRing,        // [3][kRing] the V tile may be read
     kBarSFull = kBarClean + 3 * kRing,      // [2 slots][2 halves]
     kBarPFull = kBarSFull + 4,              // [2][2]
-    kBarPvDone = kBarPFull + 4,             // [2] every P V product
+    kBarPvDone = kBarPFull + 4,             // [2] every P V product but an item's last
     kBarOFull = kBarPvDone + 2,             // [2] an item's last one
     kBarOEmpty = kBarOFull + 2,             // [2]
     kBarStatFull = kBarOEmpty + 2,          // [2]
@@ -92,7 +92,7 @@ enum : uint32_t {
     kBarDrain = kBarStatEmpty + 2,          // [2]
     kBarCount = kBarDrain + 2
 };
-static_assert(kBarCount * 8 + 16 <= 560, "barriers, TMEM address and abort flag");
+static_assert(kBarCount * 8 + 16 <= 592, "barriers, TMEM address and abort flag");
 
 // One entry of the work list: up to 2 R tokens of a sequence.
 struct Entry {
@@ -141,6 +141,7 @@ struct Params {
     int self;            // the CTAs find their work themselves (few sequences, see launch_kind)
     float *part;         // [2 grid][part_rows](max, sum) then [part_rows][128]
     int part_rows;
+    int wide;            // o's rows are aligned to 32 bytes
     unsigned *err;
 };
 
@@ -303,6 +304,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+// 32 bytes in one store where the rows are aligned to that: a warp writes a
+// piece of 32 rows at a time, a line each, whatever a piece's size
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], int wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 // 128-byte-swizzled operand descriptor (see mq_ptx.cuh) with both byte offsets
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
@@ -402,31 +416,32 @@ __device__ const __nv_bfloat16 *new_value_row(const Params &p, const Item &w, in
 }
 
 // The new tokens' K and V rows to their slots, one warp per token and KV head
-// at a time (16 lanes for K, 16 for V), `n` warps in all.
-__device__ __forceinline__ void append_rows(const PagedAttnArgs &a, int64_t w, int64_t n, int lane) {
+// at a time (16 lanes for K, 16 for V): rows w, w + n, .. of `total`, kAppend of
+// them in flight a call.
+constexpr int kAppend = 4;
+__device__ __forceinline__ int64_t append_total(const PagedAttnArgs &a) {
+    return static_cast<int64_t>(max(min(a.T, a.cu[a.B]), 0)) * a.Hkv;
+}
+__device__ __forceinline__ void append_rows(const PagedAttnArgs &a, int64_t w, int64_t n, int64_t total, int lane) {
     const int64_t n_slots = a.n_pages << a.ps_shift;
-    const int64_t total = static_cast<int64_t>(max(min(a.T, a.cu[a.B]), 0)) * a.Hkv;
-    constexpr int kU = 4;                          // rows in flight
-    for (; w < total; w += kU * n) {
-        uint4 v[kU];
-        int64_t dst[kU];
+    uint4 v[kAppend];
+    int64_t dst[kAppend];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            dst[u] = -1;
-            const int64_t x = w + u * n;
-            if (x >= total) continue;
-            const int64_t t = x / a.Hkv, g = x % a.Hkv;
-            const int64_t slot = a.slots[t];
-            if (slot < 0 || slot >= n_slots) continue;
-            dst[u] = ((((slot >> a.ps_shift) * a.Hkv + g) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * kD;
-            v[u] = reinterpret_cast<const uint4 *>(a.qkv + t * a.ldqkv + (a.H + g) * kD +
-                                                   (lane < 16 ? 0 : a.Hkv * kD))[lane & 15];
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (dst[u] >= 0)
-                reinterpret_cast<uint4 *>((lane < 16 ? a.k_pages : a.v_pages) + dst[u])[lane & 15] = v[u];
+    for (int u = 0; u < kAppend; ++u) {
+        dst[u] = -1;
+        const int64_t x = w + u * n;                // (< 2^32)
+        if (x >= total) continue;
+        const unsigned t = static_cast<unsigned>(x) / a.Hkv, g = static_cast<unsigned>(x) % a.Hkv;
+        const int64_t slot = a.slots[t];
+        if (slot < 0 || slot >= n_slots) continue;
+        dst[u] = ((((slot >> a.ps_shift) * a.Hkv + g) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * kD;
+        v[u] = reinterpret_cast<const uint4 *>(a.qkv + t * a.ldqkv + (a.H + g) * kD +
+                                               (lane < 16 ? 0 : a.Hkv * kD))[lane & 15];
     }
+#pragma unroll
+    for (int u = 0; u < kAppend; ++u)
+        if (dst[u] >= 0)
+            reinterpret_cast<uint4 *>((lane < 16 ? a.k_pages : a.v_pages) + dst[u])[lane & 15] = v[u];
 }
 
 // ---- the work list -----------------------------------------------------------------
@@ -473,8 +488,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
     griddep_wait();
     griddep_launch_dependents();
     if (kPaged && blockIdx.x > 0) {
-        append_rows(a, static_cast<int64_t>(blockIdx.x - 1) * (kPrepThreads / 32) + (tid >> 5),
-                    static_cast<int64_t>(gridDim.x - 1) * (kPrepThreads / 32), lane);
+        const int64_t n = static_cast<int64_t>(gridDim.x - 1) * (kPrepThreads / 32), total = append_total(a);
+        for (int64_t w = static_cast<int64_t>(blockIdx.x - 1) * (kPrepThreads / 32) + (tid >> 5); w < total; w += kAppend * n)
+            append_rows(a, w, n, total, lane);
         return;
     }
     const int TB = 2 * p.R;
@@ -818,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(B(kBarPFull + 2 * s + x));
             }
             if (!ok) break;
-            n_pv += 2 * c;
+            if (c) n_pv += 2 * c - 1;
             if (c) {
                 ok = __all_sync(0xFFFFFFFFu, wait(B(kBarOFull + s), n_o++ & 1));
                 if (!ok) break;
@@ -840,8 +856,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kOCol;
-        if (!kPaged && p.a.slots && !dead)
-            append_rows(p.a, static_cast<int64_t>(blockIdx.x) * 4 + quarter, static_cast<int64_t>(gridDim.x) * 4, lane);
+        // Packed prompts: the cache rows are written while an item's result is
+        // awaited (all of them at the start held up the first items of each CTA
+        // by 100 us in a batch of 14681 tokens of 8 KV heads), the rest at the end.
+        int64_t app = static_cast<int64_t>(blockIdx.x) * 4 + quarter;
+        const int64_t app_n = static_cast<int64_t>(gridDim.x) * 4;
+        const int64_t app_total = !kPaged && p.a.slots && !dead ? append_total(p.a) : 0;
+        auto append = [&]() {
+            append_rows(p.a, app, app_n, app_total, lane);
+            app += kAppend * app_n;
+        };
         __nv_bfloat162 amax2 = __floats2bfloat162_rn(0.0f, 0.0f);
         bool ok = !dead;
         for (uint32_t it = 0; ok; ++it) {
@@ -854,6 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool both = w.dual != 0;
                 if (both && s == 1) break;
                 for (int q = s; q < (both ? 2 : s + 1) && ok; ++q) {
+                    if (!kPaged)
+                        while (app < app_total && !__all_sync(0xFFFFFFFFu, mbar_test_wait(B(kBarStatFull + q), it & 1))) append();
                     ok = __all_sync(0xFFFFFFFFu, wait(B(kBarStatFull + q), it & 1));
                 }
                 if (!ok) break;
@@ -919,10 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 8; ++e)
                                 amax2 = __hmax2(amax2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[e])));
                         }
-                        if (valid) {
-                            reinterpret_cast<uint4 *>(orow + 16 * c)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                            reinterpret_cast<uint4 *>(orow + 16 * c)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                        }
+                        if (valid) store32(orow + 16 * c, pk, p.wide);
                         __syncwarp();
                     }
                 }
@@ -965,8 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (p.a.o_amax) amax2 = __hmax2(amax2, __habs2(b));
                             pk[e] = *reinterpret_cast<const uint32_t *>(&b);
                         }
-                        reinterpret_cast<uint4 *>(orow + 16 * c)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                        reinterpret_cast<uint4 *>(orow + 16 * c)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                        store32(orow + 16 * c, pk, p.wide);
                     }
                     __syncwarp();
                 }
@@ -982,6 +1004,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(B(kBarWorkEmpty + wi));
         }
+        if (!kPaged)
+            while (ok && app < app_total) append();
         if (p.a.o_amax) {
             const float amax = fmaxf(__bfloat162float(amax2.x), __bfloat162float(amax2.y));
             const unsigned u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
@@ -1065,12 +1089,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         warp_mma4_ts<kStep>(tO, tS + 64, vd + 4 * kStep, idesc_o, 1);
-                        warp_commit(B(kBarPvDone + s));
+                        warp_commit(B(more ? kBarPvDone + s : kBarOFull + s));     // (an item's last: OFull alone)
                         warp_commit(B(kBarKvEmpty + vs));
                         if (alone(i)) warp_commit(B(kBarKvEmpty + vs));
-                        if (!more) {
-                            warp_commit(B(kBarOFull + s));
-                        } else {
+                        if (more) {
                             if (!early) {
                                 ok = wwait(B(kBarKFull + kb), kpar);
                                 if (!ok) break;
@@ -1260,29 +1282,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lo < kKeys) {
                         const uint32_t tile = s0 + kRingOff + vs * kTileBytes;
                         const int end = min(max(kv_len - j * kKeys, 0), kKeys);
-                        bool found = false;
-                        for (int i = min(lo, end) * 16 + lane; i < kKeys * 16; i += 32) {
-                            const uint32_t addr = tile + L::chunk(i >> 4, i & 15);
-                            if ((i >> 4) >= end) {
-                                st_shared_v4(addr, 0, 0, 0, 0);
-                                continue;
-                            }
-                            uint32_t v[4];
-                            ld_shared_v4(addr, v);
-                            bool any = false;
+                        // rows behind the last key are zeroed, those before it
+                        // looked over
+                        const int behind = kKeys;
+#pragma unroll 1
+                        for (int i = end * 16 + lane; i < behind * 16; i += 32)
+                            st_shared_v4(tile + L::chunk(i >> 4, i & 15), 0, 0, 0, 0);
+                        __nv_bfloat162 big = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll 1
+                        for (int i0 = lo * 16 + lane; i0 < end * 16; i0 += 128) {
+                            uint32_t v[4][4];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const bool lo_bad = (v[q] & 0x7F80u) == 0x7F80u, hi_bad = (v[q] & 0x7F800000u) == 0x7F800000u;
-                                if (lo_bad) v[q] &= 0xFFFF0000u;
-                                if (hi_bad) v[q] &= 0x0000FFFFu;
-                                any = any || lo_bad || hi_bad;
+                            for (int u = 0; u < 4; ++u) {
+                                const int i = min(i0 + 32 * u, end * 16 - 1);
+                                ld_shared_v4(tile + L::chunk(i >> 4, i & 15), v[u]);
                             }
-                            if (any) {
-                                st_shared_v4(addr, v[0], v[1], v[2], v[3]);
-                                found = true;
-                            }
+#pragma unroll
+                            for (int u = 0; u < 4 * 4; ++u)
+                                big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[u >> 2][u & 3])));
                         }
-                        if (__any_sync(0xFFFFFFFFu, found) && lane == 0) items[wi].bad = 1;
+                        const uint32_t seen = *reinterpret_cast<const uint32_t *>(&big);
+                        if (__any_sync(0xFFFFFFFFu, (seen & 0x7F80u) == 0x7F80u || (seen & 0x7F800000u) == 0x7F800000u)) {
+#pragma unroll 1
+                            for (int i = lo * 16 + lane; i < end * 16; i += 32) {
+                                const uint32_t addr = tile + L::chunk(i >> 4, i & 15);
+                                uint32_t v[4];
+                                ld_shared_v4(addr, v);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    if ((v[q] & 0x7F80u) == 0x7F80u) v[q] &= 0xFFFF0000u;
+                                    if ((v[q] & 0x7F800000u) == 0x7F800000u) v[q] &= 0x0000FFFFu;
+                                }
+                                st_shared_v4(addr, v[0], v[1], v[2], v[3]);
+                            }
+                            if (lane == 0) items[wi].bad = 1;
+                        }
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
@@ -1488,6 +1522,7 @@ cudaError_t launch_attention_paged(const PagedAttnArgs &a, void *ws, unsigned *e
     p.grid = grid;
     p.part = reinterpret_cast<float *>(base + w.part);
     p.part_rows = w.part_rows;
+    p.wide = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.ldo % 16 == 0;
     p.err = err;
     CUtensorMap tq, tk, tv;
     const cuuint64_t ld = static_cast<cuuint64_t>(a.ldqkv) * 2;
