@@ -397,12 +397,15 @@ __device__ __forceinline__ int entry_tiles(const Entry &e, int64_t cap) {
     return static_cast<int>((min(static_cast<int64_t>(e.pos0) + e.ntok, cap) + kKeys - 1) / kKeys);
 }
 
-// Cost of one of its tiles: with queries in both slots twice that of a tile
-// that one slot takes while the other takes the next (alone 2.6 and 1.1 us, but
-// among others the first is held up less; four chunks beside 60 single tokens:
-// 440 us at equal cost, 361 at 2 : 1, 386 at 7 : 4, 396 at 5 : 2).
-constexpr int kCostTwo = 2, kCostOne = 1;
+// Cost of one of an entry's tiles, and of an item besides its tiles, in eighths
+// of a tile that one slot takes while the other takes the next.  Measured over
+// the CTAs of four chunks beside 60 single tokens: 2.1 us a tile with queries in
+// both slots, 1.3 us a tile that they share, 2 and 2.8 us an item (its first
+// loads and its epilogue); with these costs the whole call takes 349 us, with
+// 2 : 1 for the tiles alone 397, with 7 : 4 alone 379.
+constexpr int kCostTwo = 13, kCostOne = 8, kCostItemTwo = 12, kCostItemOne = 18;
 __device__ __forceinline__ int tile_cost(const Entry &e, int R) { return e.ntok > R ? kCostTwo : kCostOne; }
+__device__ __forceinline__ int item_cost(const Entry &e, int R) { return e.ntok > R ? kCostItemTwo : kCostItemOne; }
 
 // V of a new token i of the entry (for the rows that a cleaned value belongs to)
 template <bool kPaged>
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
             if (e < n_ent) {
                 const Entry r = entry(e, tiles);
                 p.ent[e] = r;
-                cost = tiles * tile_cost(r, p.R);
+                cost = tiles ? item_cost(r, p.R) + tiles * tile_cost(r, p.R) : 0;
             }
             int64_t total;
             const int64_t at = block_scan(cost, red, &total);
@@ -552,7 +555,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
         // the ranges: equal shares of the cost of all entries and heads; a border
         // inside an entry falls on its next whole tile
         const int64_t W = at0 * a.Hkv;
-        // (a share holds one whole tile at least, so no range is empty)
+        // (a share holds one whole tile at least, so no range inside an item is
+        // empty; one between items may be)
         const int64_t most = min(W, max(W / (a.max_new > p.R ? kCostTwo : kCostOne), static_cast<int64_t>(1)));
         const int n = static_cast<int>(min(most, static_cast<int64_t>(p.grid)));
         struct Place {
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
             r.e = lo;
             const Entry en = p.ent[lo];
             const int u = tile_cost(en, p.R);
-            r.t = static_cast<int>((y - p.prefix[lo] + u - 1) / u);
+            r.t = static_cast<int>(max((y - p.prefix[lo] - item_cost(en, p.R) + u - 1) / u, static_cast<int64_t>(0)));
             if (r.t >= entry_tiles(en, cap)) {   // the entry's end: the next one with tiles
                 r.t = 0;
                 do {
@@ -600,7 +604,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
                     r.cut_g = hi.g;
                     // the first border past its last tile's start, less one
                     const int u = tile_cost(r.cut, p.R);
-                    const int64_t x = hi.g * at0 + p.prefix[hi.e] + static_cast<int64_t>(entry_tiles(r.cut, cap) - 1) * u + 1;
+                    const int64_t x = hi.g * at0 + p.prefix[hi.e] + item_cost(r.cut, p.R) +
+                                      static_cast<int64_t>(entry_tiles(r.cut, cap) - 1) * u + 1;
                     r.cut_to = static_cast<int>(min((x * n + W - 1) / W, static_cast<int64_t>(n))) - 1;
                 }
             } else {
