@@ -449,8 +449,10 @@ __device__ __forceinline__ void append_rows(const PagedAttnArgs &a, int64_t w, i
 
 // ---- the work list -----------------------------------------------------------------
 
+constexpr int kMaxCtas = 160;       // the launch uses no more: ranges and partial results have this many places
 constexpr int kPrepThreads = 1024;
 constexpr int kBins = 4096;
+constexpr int kFewSums = 1024;
 
 // Exclusive prefix sum over the block; *total gets the sum.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *red, int64_t *total) {
@@ -536,6 +538,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
         return r;
     };
     if (kPaged) {
+        // (the search for the borders reads few sums from shared memory)
+        __shared__ int64_t few[kFewSums];
+        int64_t *const pre = n_ent < kFewSums ? few : p.prefix;
         int64_t at0 = 0;
         for (int e0 = 0; e0 < n_ent; e0 += kPrepThreads) {
             const int e = e0 + tid;
@@ -547,10 +552,10 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
             }
             int64_t total;
             const int64_t at = block_scan(cost, red, &total);
-            if (e < n_ent) p.prefix[e] = at0 + at;
+            if (e < n_ent) pre[e] = at0 + at;
             at0 += total;
         }
-        if (tid == 0) p.prefix[n_ent] = at0;
+        if (tid == 0) pre[n_ent] = at0;
         __syncthreads();
         // the ranges: equal shares of the cost of all entries and heads; a border
         // inside an entry falls on its next whole tile
@@ -570,12 +575,12 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
             int lo = 0, hi = n_ent;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (p.prefix[mid] <= y) lo = mid; else hi = mid;
+                if (pre[mid] <= y) lo = mid; else hi = mid;
             }
             r.e = lo;
             const Entry en = p.ent[lo];
             const int u = tile_cost(en, p.R);
-            r.t = static_cast<int>(max((y - p.prefix[lo] - item_cost(en, p.R) + u - 1) / u, static_cast<int64_t>(0)));
+            r.t = static_cast<int>(max((y - pre[lo] - item_cost(en, p.R) + u - 1) / u, static_cast<int64_t>(0)));
             if (r.t >= entry_tiles(en, cap)) {   // the entry's end: the next one with tiles
                 r.t = 0;
                 do {
@@ -583,14 +588,17 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
                         r.e = 0;
                         ++r.g;
                     }
-                } while (r.g < a.Hkv && p.prefix[r.e + 1] == p.prefix[r.e]);
+                } while (r.g < a.Hkv && pre[r.e + 1] == pre[r.e]);
             }
             return r;
         };
+        __shared__ Place border[kMaxCtas + 1];
+        for (int c = tid; c <= n; c += kPrepThreads) border[c] = c < n ? locate(c) : Place{0, a.Hkv, 0};
+        __syncthreads();
         for (int c = tid; c < p.grid; c += kPrepThreads) {
             Range r = {};
             if (c < n) {
-                const Place lo = locate(c), hi = c + 1 < n ? locate(c + 1) : Place{0, a.Hkv, 0};
+                const Place lo = border[c], hi = border[c + 1];
                 r.e = lo.e;
                 r.g = lo.g;
                 r.t0 = lo.t;
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
                     r.cut_g = hi.g;
                     // the first border past its last tile's start, less one
                     const int u = tile_cost(r.cut, p.R);
-                    const int64_t x = hi.g * at0 + p.prefix[hi.e] + item_cost(r.cut, p.R) +
+                    const int64_t x = hi.g * at0 + pre[hi.e] + item_cost(r.cut, p.R) +
                                       static_cast<int64_t>(entry_tiles(r.cut, cap) - 1) * u + 1;
                     r.cut_to = static_cast<int>(min((x * n + W - 1) / W, static_cast<int64_t>(n))) - 1;
                 }
@@ -1468,8 +1476,6 @@ Workspace carve(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv, b
 
 }  // namespace
 
-// (partial results for up to this many CTAs; the launch uses no more)
-constexpr int kMaxCtas = 160;
 
 size_t attention_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_new, int64_t H, int64_t Hkv, bool paged) {
     return carve(T, B, max_new, H, Hkv, paged, kMaxCtas).total;
