@@ -19,8 +19,19 @@
 // slots the same queries and every other K / V tile; their two results are
 // merged in the epilogue, so a decode step keeps two tiles in flight too.
 //
+// A slot takes a K / V tile as two halves of 64 keys with an S buffer each:
+// P V of a half, then S of the next tile's same half over it, while the softmax
+// is at the other half (8192-token prompt 537 us; tiles of 128 keys at a time,
+// where P, P V and the next S are one chain, 697 us; the halves cost the tensor
+// cores 392 instead of 256 cycles for each S, as Q crosses shared memory twice).
+//
 // Warps: 0-3 / 4-7 softmax of slot 0 / 1 (a thread per row), 8-11 epilogue,
 // 12 / 13 MMA issue of slot 0 / 1, 14 work list and TMA, 15 cleans V tiles.
+//
+// Roundings: P to BF16 for its product (the sum that divides is of the unrounded
+// weights), o to BF16; scores, maxima, sums and o's accumulation are FP32.  The
+// running maximum is raised for growths beyond 2^8 only, which keeps weights
+// below 2^8 and costs nothing in precision, as they are floating point.
 //
 // Cleaning: P is 0 at a masked key, but 0 x NaN is NaN, and what lies behind a
 // sequence's last key (unwritten cache rows, another sequence, padding) may be
@@ -29,12 +40,26 @@
 // for others) is zeroed too and added again, row by row, in the epilogue.
 //
 // Work.  Packed prompts: items sorted by length, heaviest first over all heads,
-// taken from a counter (8192 tokens, 8 KV heads: 573 us; one head after the
-// other 617 us, for its last long items; no better where the keys of all heads
-// are larger than L2 either).  Paged: the K / V
-// tiles of all items in a row, cut into one equal range per CTA; an item cut
-// by a border leaves (max, sum, unnormalised o) of its parts, merged by a
-// second kernel, so one long sequence fills the GPU as well as many do.
+// taken from a counter (one head after the other ended with its long items:
+// 617 against 573 us for 8192 tokens of 8 KV heads when it was tried, and no
+// better where the keys of all heads are larger than L2).  Paged: the K / V
+// tiles of all items in a row, cut into one range of equal cost per CTA; an
+// item cut by a border leaves (max, sum, unnormalised o) of its parts, merged
+// by a second kernel, so one long sequence fills the GPU as well as many do
+// (merged by the CTA that ends last instead: 462 against 374 us for four chunks
+// beside 60 single tokens, its one SM reads the parts of up to 256 rows).
+//
+// What bounds it.  Prompts and chunks: the softmax.  A half takes its warp 1450
+// cycles among the others (650 alone in a loop by itself, 1150 with a second
+// warp on the scheduler and products running), the two slots' products 1300;
+// with the hand-overs 1760 a half, so the tensor pipe does its products in half
+// of the cycles (8192 tokens, 32 / 8 heads: 537 us, 1.02 PFLOP/s; 16384 tokens
+// over 49152: 16.0 ms, 0.96; the GPU is at its power limit there, 1.6 to 1.75
+// GHz).  Short prompts: 2.3 us from an item's last P to the next one's first S
+// and its epilogue of 2 us a slot (16 prompts of 64 to 4096 tokens, 64 / 8
+// heads: 431 us, 0.76 PFLOP/s).  Single tokens: the cache's bytes (64 of 512 to
+// 8192 positions, 667 MB: 126 us, 5.3 TB/s; one of 32768 39 us, 3.4 TB/s; one
+// of 8192 23 us, of which the two other kernels take 8).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -210,10 +235,10 @@ __device__ __forceinline__ void exp2_pair_fma(uint64_t x, float &y0, float &y1) 
 // Weights of 32 scores to the base 2^-nm as BF16 pairs, their sum (of the
 // unrounded weights) added to lp.  Of each 16 pairs kExpFma take the FMA pipes:
 // the transcendental unit (16 a clock per SM) needs as long for a tile's
-// exponentials as the tensor cores for its products.  Measured with 0 / 3 / 4 /
-// 5 / 6 of 16: 16384 tokens over 49152 17.7 / 16.9 / 16.3 / 16.1 / 16.6 ms,
-// 8192-token prompt 581 / 571 / 562 / 557 / 570 us, ragged prompts 519 / 523 /
-// 527 / 529 / 535 us, 64 decode rows 129 / - / 131 / 134 / - us.
+// exponentials as the tensor cores for its products.  Measured with 3 / 4 /
+// 5 / 6 of 16: 8192-token prompt 550 / 537 / 544 / 539 us, ragged prompts 449 /
+// 450 / 453 / 459 us, 64 single tokens 161 / 163 / 165 / 166 us (with none, the
+// prompt took 581 us where 4 took 562).
 constexpr int kExpFma = 4;
 __device__ __forceinline__ void weights32(const float *s, float nm, uint32_t (&pk)[16], uint64_t (&lp)[2]) {
     const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), nm2 = pack2(nm, nm);
@@ -483,7 +508,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *red, int64_t *
 
 // Block 0 makes the work list; with a paged cache the other blocks meanwhile
 // write the new tokens' rows to it (packed prompts: the attention kernel does,
-// as nothing there reads the cache).
+// as nothing there reads the cache).  A few KB of lengths in one block's scans
+// and searches: latency, 4 us for one sequence to 8 us for 64; the rows are
+// copied in the same time (3349 tokens of 8 KV heads, 27 MB: 12 us cold).
 template <bool kPaged>
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p) {
     extern __shared__ int offs[];                  // [B + 1] entries before each sequence; packed: then kBins bins
@@ -686,6 +713,7 @@ struct SelfPlan {
     }
 };
 
+// (bounds, rates and the roles of the warps: at the top of the file)
 template <bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -1357,6 +1385,9 @@ constexpr int kCombineRows = 8;       // rows a block takes at a time: a warp ea
 
 // Block (c, y): the item that begins in CTA c's range and goes on past it.
 // Its parts: c's second place, then the first place of the CTAs after c.
+// Latency of three dependent reads, 5 to 7 us cold; with chunks 39 MB of parts
+// lie in L2 (20 us for 148 cut items; half a warp a row takes 14, but 2 us more
+// where a row has many parts).
 __global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const Params p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PagedAttnArgs &a = p.a;
@@ -1492,8 +1523,8 @@ static cudaError_t launch_kind(Params &p, const CUtensorMap &tq, const CUtensorM
     e = cudaFuncSetAttribute(paged_attention_kernel<kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     // Few short prompts: no work list (three of 348 tokens in all: 16.3 against
-    // 19.3 us with it; paged calls gained nothing, their list kernel also writes
-    // the new cache rows).
+    // 19.3 us with it when that was tried, 11.8 now; paged calls gained nothing,
+    // their list kernel also writes the new cache rows).
     p.self = !kPaged && a.B <= 32 && (a.T / (2 * p.R) + a.B) * static_cast<int64_t>(a.Hkv) <= grid;
     if (p.self) {
         if (a.o_amax && (e = cudaMemsetAsync(a.o_amax, 0, sizeof(float), s)) != cudaSuccess) return e;
