@@ -49,13 +49,14 @@
 // (merged by the CTA that ends last instead: 462 against 374 us for four chunks
 // beside 60 single tokens, its one SM reads the parts of up to 256 rows).
 //
-// What bounds it.  Prompts and chunks: the softmax.  A half takes its warp 1450
-// cycles among the others (650 alone in a loop by itself, 1150 with a second
-// warp on the scheduler and products running), the two slots' products 1300;
-// with the hand-overs 1760 a half, so the tensor pipe does its products in half
-// of the cycles (8192 tokens, 32 / 8 heads: 537 us, 1.02 PFLOP/s; 16384 tokens
-// over 49152: 16.0 ms, 0.96; the GPU is at its power limit there, 1.6 to 1.75
-// GHz).  Short prompts: 2.3 us from an item's last P to the next one's first S
+// What bounds it.  Prompts and chunks: the hand-overs between softmax and
+// products, and power.  A half takes its softmax warp 1450 cycles among the
+// others and 300 of waiting for S, the two slots' products 1300, so the tensor
+// pipe does its products in half of the cycles (8192 tokens, 32 / 8 heads: 537
+// us, 1.02 PFLOP/s; 16384 tokens over 49152: 16.0 ms, 0.96).  A copy without
+// the exponentials gains 2%: the GPU is at its 1000 W (32768 tokens: 8.4 ms at
+// 1.56 GHz; the products alone, without any softmax, 7.0 ms at 1.63 GHz).
+// Short prompts: 2.3 us from an item's last P to the next one's first S
 // and its epilogue of 2 us a slot (16 prompts of 64 to 4096 tokens, 64 / 8
 // heads: 431 us, 0.76 PFLOP/s).  Single tokens: the cache's bytes (64 of 512 to
 // 8192 positions, 667 MB: 126 us, 5.3 TB/s; one of 32768 39 us, 3.4 TB/s; one
