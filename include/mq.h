@@ -365,10 +365,11 @@ mq_status mq_attention_decode_bf16(const void *qkv_bf16, int64_t m, int64_t pos0
  *     all others left as they are;
  *   slots [T] (int64): the cache slot of each row; -1 for rows past cu_new[B]
  *     and for tokens that got no page (free_pages or the table row is used
- *     up, or the table names a negative page);
- *   info [4] (int32): new tokens asked for, pages needed (the first info[1]
- *     of free_pages are now in use), tokens of the first count without a slot
- *     (cut at T, or without a page), and the longest ctx + new.
+ *     up, or the table or free_pages names a negative page);
+ *   info [4] (int32): new tokens asked for, pages needed (the first of
+ *     free_pages, as many as that or all n_free, are now in use), tokens of
+ *     the first count without a slot (cut at T, or without a page), and the
+ *     longest ctx + new (the tokens past T left out).
  * Errors: MQ_ERR_INVALID_ARG (null pointer), MQ_ERR_SHAPE (B, T, page_size,
  * max_pages out of range), MQ_ERR_ALIGNMENT (natural alignment). */
 mq_status mq_paged_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,

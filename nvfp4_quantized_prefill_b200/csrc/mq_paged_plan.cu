@@ -6,14 +6,18 @@
 //   table[b][held_b + j] = free[sum_{i < b} need_i + j]       (j < need_b)
 //   slot(t)          = table[b][pos / ps] * ps + pos % ps,  pos = ctx_b + t - cu[b]
 //
-// At most about 1 MB is read and written, so the launch is what it costs.  One
-// kernel does it all: every block takes both prefix sums over the requests by
-// itself (the lengths are a few KB, in L2 after the first block; a thread keeps
-// its run of consecutive requests in registers) and leaves them in shared
-// memory, then fills its own token rows, so no block waits for another.  A new
-// page's table entry is written by the thread of the page's first token.
-// Measured (graph replays): 4.3 us for 8 requests, 8.9 us for 4096 requests
-// with 114009 tokens (1.0 MB).
+// 8 bytes are written per row and little else is moved (1.0 MB for 4096 requests
+// with 114009 rows), so the launch is what it costs.  One kernel does it all:
+// every block takes both prefix sums over the requests by itself (the lengths are
+// a few KB, in L2 after the first block; a thread keeps its run of consecutive
+// requests in registers) and leaves them in shared memory, then fills its own
+// token rows, so no block waits for another.  Where there are several, the first
+// block fills none: it looks for negative ids in the table and the free list and
+// counts the tokens without a slot (16 loads a thread in flight: with 4, 262144
+// pages of one step took it 86 us, twice the others' time).  A new page's table
+// entry is written by the thread of the page's first token.
+// Measured, us a call among 40 in a graph: 2.3 for 8 requests, 3.5 for 257, 6.9
+// for 4096 with 114009 rows, 34 for 16384, 43 for 2.1 million rows in pages of 8.
 #include <algorithm>
 
 #include "mq_internal.h"
@@ -80,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
     griddep_launch_dependents();
     const int b0 = min(tid * kPer, p.B), nb = min(kPer, p.B - b0);
     const int ps = 1 << p.ps_shift;
-    const int64_t T = p.T, most = p.max_pages;
+    const int64_t T = p.T;
     int ctx[kPer], nw[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -91,13 +95,16 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
         lost_s = 0;
         longest_s = 0;
     }
-    auto pages_to = [&](int64_t n) { return min((n + ps - 1) >> p.ps_shift, most); };   // that a table row can hold
+    // (unsigned 32 bits hold a length cut at T: below 2^31 + 2^22)
+    const unsigned most = p.max_pages;
+    auto pages_of = [&](unsigned n) { return (n + ps - 1) >> p.ps_shift; };
+    auto pages_to = [&](unsigned n) { return min(pages_of(n), most); };         // that a table row can hold
     // both sums at once, as if no row were cut at T; the pages again if some are
     int64_t at = 0, base = 0, asked, pages;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         at += nw[i];
-        base += pages_to(static_cast<int64_t>(ctx[i]) + nw[i]) - pages_to(ctx[i]);
+        base += pages_to(static_cast<unsigned>(ctx[i]) + nw[i]) - pages_to(ctx[i]);
     }
     block_scan2<kThreads>(at, base, red, asked, pages);
     if (asked > T) {
@@ -105,36 +112,76 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
         base = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int64_t lo = min(a, T), hi = min(a + nw[i], T);
+            const int lo = static_cast<int>(min(a, T)), hi = static_cast<int>(min(a + nw[i], T));
             a += nw[i];
-            base += pages_to(ctx[i] + (hi - lo)) - pages_to(ctx[i]);
+            base += pages_to(static_cast<unsigned>(ctx[i]) + (hi - lo)) - pages_to(ctx[i]);
         }
         block_scan2<kThreads>(none, base, red, zero, pages);
     }
-    int longest = 0;
+    // tokens past the pages that a request has and gets have no slot
+    int lost = 0;
+    unsigned longest = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (i >= nb) break;
-        const int64_t lo = min(at, T), hi = min(at + nw[i], T), end = ctx[i] + (hi - lo);
+        const int lo = static_cast<int>(min(at, T)), hi = static_cast<int>(min(at + nw[i], T));
+        const unsigned c = ctx[i], end = c + (hi - lo), held = pages_to(c), need = pages_to(end) - held;
         ctx_s[b0 + i] = ctx[i];
-        cu_s[b0 + i] = static_cast<int>(lo);
+        cu_s[b0 + i] = lo;
         base_s[b0 + i] = static_cast<int>(base);
-        base += pages_to(end) - pages_to(ctx[i]);
+        const unsigned have = held + static_cast<unsigned>(min(static_cast<int64_t>(need), max(p.n_free - base, static_cast<int64_t>(0))));
+        if (have < pages_of(end)) lost += end - max(c, have << p.ps_shift);
+        base += need;
         at += nw[i];
-        longest = max(longest, static_cast<int>(min(end, static_cast<int64_t>(INT32_MAX))));
+        longest = max(longest, end);
     }
     if (tid == 0) cu_s[p.B] = static_cast<int>(min(asked, T));
     __syncthreads();
     if (blockIdx.x == 0) {
-        // the prefix of rows, and what the caller has to know of the step
-        int lost = 0;
-        for (int b = b0; b < b0 + nb; ++b) {
-            const int64_t c = ctx_s[b], end = c + (cu_s[b + 1] - cu_s[b]), held = pages_to(c);
-            const int64_t got = min(pages_to(end) - held, max(static_cast<int64_t>(p.n_free) - base_s[b], static_cast<int64_t>(0)));
-            lost += static_cast<int>(end - min(end, max(c, (held + got) << p.ps_shift)));
+        // the prefix of rows, and what the caller has to know of the step: also
+        // without a slot are tokens whose page has a negative id, in the table
+        // (the last page held, if it is not full) or in the free list
+        constexpr int kFlight = 16;            // loads in flight
+        for (int j0 = tid; j0 < p.B; j0 += kFlight * kThreads) {
+            int id[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int b = j0 + u * kThreads;
+                id[u] = 0;
+                if (u < kPer && b < p.B) {
+                    const unsigned c = ctx_s[b], page = c >> p.ps_shift;
+                    if (cu_s[b + 1] > cu_s[b] && (c & (ps - 1)) && page < most) id[u] = p.table[static_cast<int64_t>(b) * most + page];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (id[u] < 0) {
+                    const int b = j0 + u * kThreads;
+                    lost += min(cu_s[b + 1] - cu_s[b], ps - (ctx_s[b] & (ps - 1)));
+                }
+        }
+        const int taken = static_cast<int>(min(pages, static_cast<int64_t>(p.n_free)));
+        for (int k0 = tid; k0 < taken; k0 += kFlight * kThreads) {
+            int id[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) id[u] = u * kThreads < taken - k0 ? p.free_pages[k0 + u * kThreads] : 0;
+            unsigned neg = 0;
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) neg |= (id[u] < 0 ? 1u : 0u) << u;
+            for (; neg; neg &= neg - 1) {
+                const int k = k0 + (__ffs(neg) - 1) * kThreads;
+                int lo = 0, hi = p.B;          // the last request with base[b] <= k
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (base_s[mid] <= k) lo = mid; else hi = mid;
+                }
+                const unsigned end = static_cast<unsigned>(ctx_s[lo]) + (cu_s[lo + 1] - cu_s[lo]);
+                const unsigned start = (pages_to(ctx_s[lo]) + (k - base_s[lo])) << p.ps_shift;
+                lost += min(end - start, static_cast<unsigned>(ps));
+            }
         }
         if (lost) atomicAdd(&lost_s, lost);
-        atomicMax(&longest_s, longest);
+        atomicMax(&longest_s, static_cast<int>(min(longest, static_cast<unsigned>(INT32_MAX))));
         for (int b = tid; b <= p.B; b += kThreads) p.cu[b] = cu_s[b];
         __syncthreads();
         if (tid == 0) {
@@ -146,7 +193,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
         }
     }
     const int total = cu_s[p.B];
-    for (int t = blockIdx.x * kThreads + tid; t < p.T; t += gridDim.x * kThreads) {
+    const int first = gridDim.x > 1 ? 1 : 0;       // block 0 only counts where there are others to fill the rows
+    if (static_cast<int>(blockIdx.x) < first) return;
+    for (int t = (blockIdx.x - first) * kThreads + tid; t < p.T; t += (gridDim.x - first) * kThreads) {
         int64_t slot = -1;
         if (t < total) {
             int lo = 0, hi = p.B;          // the last request with cu[b] <= t
@@ -182,7 +231,7 @@ cudaError_t launch_plan(const PlanParams &p, int num_sms, cudaStream_t s) {
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    const int grid = std::min((p.T + kThreads - 1) / kThreads, num_sms);
+    const int rows = (p.T + kThreads - 1) / kThreads, grid = rows == 1 ? 1 : std::max(std::min(rows + 1, num_sms), 2);
     const cudaError_t e = launch_pdl(paged_plan_kernel<kThreads, kPer>, dim3(grid), dim3(kThreads), smem, s, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
