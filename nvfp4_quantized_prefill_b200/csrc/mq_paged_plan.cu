@@ -227,8 +227,10 @@ template <int kThreads, int kPer>
 cudaError_t launch_plan(const PlanParams &p, int num_sms, cudaStream_t s) {
     const size_t smem = (3 * static_cast<size_t>(p.B) + 1) * sizeof(int);
     if (smem > 48 * 1024) {
+        // the same value on every call: concurrent callers cannot undo each other
+        constexpr int kMost = (3 * kThreads * kPer + 1) * sizeof(int);
         const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel<kThreads, kPer>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
     }
     const int rows = (p.T + kThreads - 1) / kThreads, grid = rows == 1 ? 1 : std::max(std::min(rows + 1, num_sms), 2);

@@ -1,12 +1,14 @@
 """Edges of the paged serving calls: plans over tables and free lists with
-negative pages."""
+negative pages, and host threads planning at once."""
 import random
+import threading
 
 import pytest
+import torch
 
 from mqtest import ensure_built
 from nvfp4_quantized_prefill_b200 import binding as mq
-from test_gpu_paged import _plan, plan_ref
+from test_gpu_paged import _i32, _plan, plan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,33 @@ def test_a_step_after_the_free_list_ran_out():
     assert slots.tolist() == [-1] * 4 and info.tolist() == [4, 1, 4, 20]
     _, slots, table, info = _plan([20], [4], ps, [], table.tolist(), 3, 4)
     assert slots.tolist() == [-1] * 4 and info.tolist() == [4, 0, 4, 24]
+
+
+def test_host_threads_plan_at_once():
+    """Calls of two sizes of shared memory from four threads, over and over."""
+    def case(B):
+        return dict(ctx=_i32([7] * B), new=_i32([1] * B), B=B, ps=8,
+                    free=torch.arange(B, dtype=torch.int32, device="cuda"), n_free=B,
+                    table=torch.full((B, 2), 5, dtype=torch.int32, device="cuda"), max_pages=2, T=B,
+                    cu=torch.zeros(B + 1, dtype=torch.int32, device="cuda"),
+                    slots=torch.zeros(B, dtype=torch.int64, device="cuda"), info=_i32([0] * 4), s=torch.cuda.Stream())
+    cases, codes = [case(B) for B in (5000, 16384, 5001, 16383)], {}
+    torch.cuda.synchronize()
+    go = threading.Barrier(len(cases))
+    plan = mq.lib().mq_paged_plan
+
+    def work(i, args):
+        go.wait(30)
+        codes[i] = {plan(*args) for _ in range(6000)}
+    threads = [threading.Thread(target=work, args=(i, [x.data_ptr() if torch.is_tensor(x) else
+                                                       x if isinstance(x, int) else x.cuda_stream for x in c.values()]))
+               for i, c in enumerate(cases)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == {i: {0} for i in range(len(cases))}, {i: [mq.STATUS[c] for c in v] for i, v in codes.items()}
+    for c in cases:
+        assert c["info"].tolist() == [c["B"], 0, 0, 8] and (c["slots"] == 47).all()
+    assert mq.mq_check() == 0
