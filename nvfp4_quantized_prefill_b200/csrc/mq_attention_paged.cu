@@ -212,10 +212,11 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
     return d;
 }
 // 2^x of a pair on the FMA and integer pipes: x = n + f with n the nearest
-// integer (read from the low bits of x + 1.5 2^23), 2^f by the cubic 1 + f (...)
-// of least relative error on [-0.5, 0.5] (1.0e-4, fitted here by Lawson
-// iteration; the result is rounded to BF16, 2e-3), n added to the exponent.
-// From -127 down (masked scores): exactly 0, as 2^0 is exactly 1.  x < 128.
+// integer (read from the low bits of x + 1.5 2^23), 2^f by the quintic 1 + f (...)
+// of least relative error on [-0.5, 0.5] (9.1e-8, fitted here by Lawson
+// iteration; 2^-22 with the roundings, as the transcendental unit's), n added to
+// the exponent.  From -127 down (masked scores): exactly 0, as 2^0 is exactly 1;
+// between -127 and -126 something below 2^-126.  x < 128.
 __device__ __forceinline__ void exp2_pair_fma(uint64_t x, float &y0, float &y1) {
     float x0, x1;
     unpack2(x, x0, x1);
@@ -223,9 +224,12 @@ __device__ __forceinline__ void exp2_pair_fma(uint64_t x, float &y0, float &y1) 
     const uint64_t t = fadd2(x, pack2(12582912.0f, 12582912.0f));
     const uint64_t n = fadd2(t, pack2(-12582912.0f, -12582912.0f));
     const uint64_t f = ffma2(n, pack2(-1.0f, -1.0f), x);
-    uint64_t p = ffma2(f, pack2(0.05500893294811249f, 0.05500893294811249f), pack2(0.24221095442771912f, 0.24221095442771912f));
-    p = ffma2(p, f, pack2(0.6932829022407532f, 0.6932829022407532f));
-    p = ffma2(p, f, pack2(1.0f, 1.0f));
+    auto twice = [](float c) { return pack2(c, c); };
+    uint64_t p = ffma2(f, twice(0.001326472731307149f), twice(0.009671512991189957f));
+    p = ffma2(p, f, twice(0.05550733581185341f));
+    p = ffma2(p, f, twice(0.24022242426872253f));
+    p = ffma2(p, f, twice(0.6931470036506653f));
+    p = ffma2(p, f, twice(1.0f));
     float t0, t1, p0, p1;
     unpack2(t, t0, t1);
     unpack2(p, p0, p1);
@@ -236,10 +240,12 @@ __device__ __forceinline__ void exp2_pair_fma(uint64_t x, float &y0, float &y1) 
 // Weights of 32 scores to the base 2^-nm as BF16 pairs, their sum (of the
 // unrounded weights) added to lp.  Of each 16 pairs kExpFma take the FMA pipes:
 // the transcendental unit (16 a clock per SM) needs as long for a tile's
-// exponentials as the tensor cores for its products.  Measured with 3 / 4 /
-// 5 / 6 of 16: 8192-token prompt 550 / 537 / 544 / 539 us, ragged prompts 449 /
-// 450 / 453 / 459 us, 64 single tokens 161 / 163 / 165 / 166 us (with none, the
-// prompt took 581 us where 4 took 562).
+// exponentials as the tensor cores for its products.  Measured with 0 / 2 / 3 /
+// 4 / 5 of 16, back to back and in turns: 8192-token prompt 581 / 562 / 559 /
+// 549 / 553 us, ragged prompts 454 / 449 / 450 / 451 / 463 us, chunks beside
+// single tokens 396 / 386 / 386 / 391 / 405 us, 64 single tokens 129 / 129 / 131
+// / 130 / 134 us (2% is within the spread: some gain, its share does not matter
+// much).
 constexpr int kExpFma = 4;
 __device__ __forceinline__ void weights32(const float *s, float nm, uint32_t (&pk)[16], uint64_t (&lp)[2]) {
     const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), nm2 = pack2(nm, nm);
