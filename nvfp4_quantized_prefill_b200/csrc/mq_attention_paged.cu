@@ -424,7 +424,8 @@ struct Layout {
 
 __device__ __forceinline__ int64_t range_begin(int64_t W, int c, int n) { return W * c / n; }
 
-// K / V tiles of an entry; cap: positions that a table row has pages for.
+// K / V tiles of an entry, one at least (an entry has a token, and a table row a
+// page); cap: positions that a table row has pages for.
 __device__ __forceinline__ int entry_tiles(const Entry &e, int64_t cap) {
     return static_cast<int>((min(static_cast<int64_t>(e.pos0) + e.ntok, cap) + kKeys - 1) / kKeys);
 }
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
             if (e < n_ent) {
                 const Entry r = entry(e, tiles);
                 p.ent[e] = r;
-                cost = tiles ? item_cost(r, p.R) + tiles * tile_cost(r, p.R) : 0;
+                cost = item_cost(r, p.R) + tiles * tile_cost(r, p.R);
             }
             int64_t total;
             const int64_t at = block_scan(cost, red, &total);
@@ -615,14 +616,12 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(const Params p
             const Entry en = p.ent[lo];
             const int u = tile_cost(en, p.R);
             r.t = static_cast<int>(max((y - pre[lo] - item_cost(en, p.R) + u - 1) / u, static_cast<int64_t>(0)));
-            if (r.t >= entry_tiles(en, cap)) {   // the entry's end: the next one with tiles
+            if (r.t >= entry_tiles(en, cap)) {   // the entry's end: the next one
                 r.t = 0;
-                do {
-                    if (++r.e == n_ent) {
-                        r.e = 0;
-                        ++r.g;
-                    }
-                } while (r.g < a.Hkv && pre[r.e + 1] == pre[r.e]);
+                if (++r.e == n_ent) {
+                    r.e = 0;
+                    ++r.g;
+                }
             }
             return r;
         };
@@ -1188,20 +1187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item w = {};
                 w.last = 1;
                 if (kPaged) {
-                    // (entries without tiles are passed over)
-                    int full = 0;
                     const int from = it == 0 ? range.t0 : 0;
-                    while (g < range.end_g || (g == range.end_g && e < range.end_e) ||
-                           (g == range.end_g && e == range.end_e && from < range.end_t)) {
-                        w.e = it == 0 && e == range.e && g == range.g ? range.first : p.ent[e];
-                        full = entry_tiles(w.e, cap);
-                        if (full > 0) break;
-                        if (++e == n_ent) {
-                            e = 0;
-                            ++g;
-                        }
-                    }
-                    if (full > 0) {
+                    if (g < range.end_g || (g == range.end_g && e < range.end_e) ||
+                        (g == range.end_g && e == range.end_e && from < range.end_t)) {
+                        w.e = it == 0 ? range.first : p.ent[e];
+                        const int full = entry_tiles(w.e, cap);
                         w.g = g;
                         w.last = 0;
                         w.t0 = from;
@@ -1332,9 +1322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int end = min(max(kv_len - j * kKeys, 0), kKeys);
                         // rows behind the last key are zeroed, those before it
                         // looked over
-                        const int behind = kKeys;
 #pragma unroll 1
-                        for (int i = end * 16 + lane; i < behind * 16; i += 32)
+                        for (int i = end * 16 + lane; i < kKeys * 16; i += 32)
                             st_shared_v4(tile + L::chunk(i >> 4, i & 15), 0, 0, 0, 0);
                         __nv_bfloat162 big = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll 1
