@@ -260,9 +260,10 @@ __global__ void __launch_bounds__(kGThreads, 2) decode_nvf4_gemv_kernel(const Ge
 template <int kM>
 cudaError_t launch_gemv(const GemvParams &p, int num_sms, cudaStream_t s) {
     const size_t smem = static_cast<size_t>(kM) * p.steps * 2048u;
+    // the same value on every call: concurrent callers cannot undo each other
     cudaError_t e = cudaFuncSetAttribute(decode_nvf4_gemv_kernel<kM>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(kDecodeGemvTokenSmem));
     if (e != cudaSuccess) return e;
     // two resident CTAs per SM, or one warp per weight row when there are fewer
     int grid = 2 * num_sms;
