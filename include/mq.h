@@ -344,12 +344,13 @@ mq_status mq_attention_decode_bf16(const void *qkv_bf16, int64_t m, int64_t pos0
  * p lies in page block_table[b][p / page_size], and slot s (int64) means row
  * s % page_size of page s / page_size.  page_size is a power of two from 8 to
  * 256; n_pages * Hkv * page_size stays below 2^34 rows and max_pages *
- * page_size within 2^30 positions.  A step's new tokens are packed: those of sequence b are rows
- * cu[b] .. cu[b + 1] - 1 of the batch (device int32 [B + 1], ascending, from
- * 0; a sequence may have none), and rows from cu[B] on (padding up to T) are
- * neither read nor written.  All lengths, tables and slots are read on the
- * device, so a captured graph can be replayed with new ones; only T, B and
- * max_new are fixed by the call. */
+ * page_size within 2^30 positions.  A step's new tokens are packed: those of
+ * sequence b are rows cu[b] .. cu[b + 1] - 1 of the batch (device int32
+ * [B + 1], ascending, from 0; a sequence may have none).  Rows from cu[B] on
+ * (padding up to T) may hold anything, affect no result, and their outputs are
+ * left as they were.  All lengths, tables and slots are read on the device, so
+ * a captured graph can be replayed with new ones; only T, B and max_new are
+ * fixed by the call. */
 
 /* Limits of B and T of the calls below. */
 #define MQ_PAGED_MAX_REQUESTS 16384
@@ -380,9 +381,12 @@ mq_status mq_paged_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_
 /* Scratch bytes of mq_attention_packed_bf16 (0 for invalid sizes). */
 size_t mq_attention_packed_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hkv, int64_t D);
 
-/* Causal attention of B packed prompts (arithmetic, head layout and limits of
+/* Causal attention of B packed prompts (formula, head layout and types of
  * mq_attention_prefill_bf16; each row attends over the rows of its own prompt
- * up to itself): qkv (device BF16, T rows of (H + 2 Hkv) * 128, leading
+ * up to itself).  BF16 products, FP32 softmax and accumulation; the weights are
+ * rounded to BF16 for their product with v, the sum that divides is of the
+ * unrounded ones, so |o - exact| <= 2^-8 (sum_j w_j |v_j| + |exact|), the FP32
+ * sums' own error aside.  qkv (device BF16, T rows of (H + 2 Hkv) * 128, leading
  * dimension ldqkv, a multiple of 8) -> o (device BF16, T rows of H * 128,
  * leading dimension ldo, a multiple of 8).  With slots (device int64 [T]; NULL
  * skips the cache, then k_pages and v_pages are NULL too) each row's keys and
@@ -414,8 +418,9 @@ size_t mq_attention_paged_workspace_bytes(int64_t T, int64_t B, int64_t max_new,
  * block_table[b] (positions past max_pages * page_size are dropped; a page
  * outside the cache reads as zeros).  qkv, o, o_amax, slots, requirements and
  * workspace as in mq_attention_packed_bf16; max_new (1 .. T) bounds the new
- * tokens of every sequence (rows beyond it are not computed) and lets the call
- * choose its launch, so pass 1 for a plain decode step. */
+ * tokens of every sequence (rows beyond it are not computed and do not count in
+ * o_amax) and lets the call choose its launch, so pass 1 for a plain decode
+ * step. */
 mq_status mq_attention_paged_bf16(const void *qkv_bf16, int64_t ldqkv, int64_t T, const int32_t *cu_new,
                                   const int32_t *ctx_lens, int64_t B, int64_t max_new, int64_t H,
                                   int64_t Hkv, int64_t D, const int64_t *slots, const int32_t *block_table,

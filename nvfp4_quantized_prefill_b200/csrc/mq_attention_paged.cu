@@ -21,17 +21,23 @@
 //
 // A slot takes a K / V tile as two halves of 64 keys with an S buffer each:
 // P V of a half, then S of the next tile's same half over it, while the softmax
-// is at the other half (8192-token prompt 537 us; tiles of 128 keys at a time,
-// where P, P V and the next S are one chain, 697 us; the halves cost the tensor
-// cores 392 instead of 256 cycles for each S, as Q crosses shared memory twice).
+// is at the other half (8192-token prompt, in one run: 537 us; tiles of 128 keys
+// at a time, where P, P V and the next S are one chain, 697 us; the halves cost
+// the tensor cores 392 instead of 256 cycles for each S, as Q crosses shared
+// memory twice).
 //
 // Warps: 0-3 / 4-7 softmax of slot 0 / 1 (a thread per row), 8-11 epilogue,
 // 12 / 13 MMA issue of slot 0 / 1, 14 work list and TMA, 15 cleans V tiles.
 //
-// Roundings: P to BF16 for its product (the sum that divides is of the unrounded
-// weights), o to BF16; scores, maxima, sums and o's accumulation are FP32.  The
-// running maximum is raised for growths beyond 2^8 only, which keeps weights
-// below 2^8 and costs nothing in precision, as they are floating point.
+// Roundings: P to BF16 for its product, o to BF16; scores, weights (2^x within
+// 2^-22), maxima, sums and o's accumulation are FP32.  The sum that divides is of
+// the unrounded weights: P's rounding then moves o by at most 2^-8 a, a = the
+// weighted |v|, and o's own by 2^-8 |o|.  (Summed from the rounded ones, as the
+// one-sequence attention does, a row with one dominant key is closer and the
+// bound 2^-8 |o| wider; it took 567 to 583 instead of 545 to 550 us for the
+// 8192-token prompt.)  The running maximum is raised for growths beyond 2^8
+// only, which keeps weights below 2^8 and costs nothing in precision, as they are
+// floating point.
 //
 // Cleaning: P is 0 at a masked key, but 0 x NaN is NaN, and what lies behind a
 // sequence's last key (unwritten cache rows, another sequence, padding) may be
@@ -41,26 +47,30 @@
 //
 // Work.  Packed prompts: items sorted by length, heaviest first over all heads,
 // taken from a counter (one head after the other ended with its long items:
-// 617 against 573 us for 8192 tokens of 8 KV heads when it was tried, and no
+// 617 against 573 us for 8192 tokens of 8 KV heads when that was tried, and no
 // better where the keys of all heads are larger than L2).  Paged: the K / V
 // tiles of all items in a row, cut into one range of equal cost per CTA; an
 // item cut by a border leaves (max, sum, unnormalised o) of its parts, merged
 // by a second kernel, so one long sequence fills the GPU as well as many do
 // (merged by the CTA that ends last instead: 462 against 374 us for four chunks
-// beside 60 single tokens, its one SM reads the parts of up to 256 rows).
+// beside 60 single tokens when that was tried, its one SM reads the parts of up to
+// 256 rows).
 //
-// What bounds it.  Prompts and chunks: the hand-overs between softmax and
-// products, and power.  A half takes its softmax warp 1450 cycles among the
+// What bounds it (rates of long runs, at 1000 W and 1.46 to 1.63 GHz; a few calls
+// after a pause take 10 to 17% less).  Prompts and chunks: the hand-overs between
+// softmax and products.  A half takes its softmax warp 1450 cycles among the
 // others and 300 of waiting for S, the two slots' products 1300, so the tensor
-// pipe does its products in half of the cycles (8192 tokens, 32 / 8 heads: 537
-// us, 1.02 PFLOP/s; 16384 tokens over 49152: 16.0 ms, 0.96).  A copy without
-// the exponentials gains 2%: the GPU is at its 1000 W (32768 tokens: 8.4 ms at
-// 1.56 GHz; the products alone, without any softmax, 7.0 ms at 1.63 GHz).
+// pipe does its products in half of the cycles (8192 tokens, 32 / 8 heads: 563
+// us, 0.98 PFLOP/s; 16384 tokens over 49152: 16.7 ms, 0.92).  The power limit
+// holds for any form and is not the reason by itself: what counts is this form's
+// energy and cycles per tile (32768 tokens: 8.4 ms at 1.56 GHz, 8.2 without the
+// exponentials, 7.0 for the products alone, without any softmax, at 1.63 GHz).
 // Short prompts: 2.3 us from an item's last P to the next one's first S
 // and its epilogue of 2 us a slot (16 prompts of 64 to 4096 tokens, 64 / 8
-// heads: 431 us, 0.76 PFLOP/s).  Single tokens: the cache's bytes (64 of 512 to
-// 8192 positions, 667 MB: 126 us, 5.3 TB/s; one of 32768 39 us, 3.4 TB/s; one
-// of 8192 23 us, of which the two other kernels take 8).
+// heads: 464 us, 0.71 PFLOP/s).  Single tokens: the cache's bytes (64 of 512 to
+// 8192 positions, 667 MB: 143 us, 4.7 TB/s, of which the list kernel and the
+// merge take 11; one of 32768 39 us, 3.4 TB/s; one of 8192 23 us, of which the
+// two other kernels take 8).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -434,8 +444,13 @@ __device__ __forceinline__ int entry_tiles(const Entry &e, int64_t cap) {
 // of a tile that one slot takes while the other takes the next.  Measured over
 // the CTAs of four chunks beside 60 single tokens: 2.1 us a tile with queries in
 // both slots, 1.3 us a tile that they share, 2 and 2.8 us an item (its first
-// loads and its epilogue); with these costs the whole call takes 349 us, with
-// 2 : 1 for the tiles alone 397, with 7 : 4 alone 379.
+// loads and its epilogue).  These are times of the CTA's work on a tile, whatever
+// the heads and pages: such a step takes, with these costs / with 2 : 1, 7 : 4 and
+// 1 : 1 for the tiles alone, 376 / 429 / 412 / 454 us (32 / 8 heads, pages of 16),
+// 235 / 257 / 249 / 294 (8 / 8 heads), 1376 / 1593 / 1470 / 1450 (64 / 8 heads,
+// pages of 64), 441 / 499 / 470 / 437 (32 / 8 heads, pages of 8: more boxes a
+// tile); two small chunks beside 98 tokens 106 / 120 / 116 / 112; 64 single
+// tokens 144 / 148 / 148 / 147.
 constexpr int kCostTwo = 13, kCostOne = 8, kCostItemTwo = 12, kCostItemOne = 18;
 __device__ __forceinline__ int tile_cost(const Entry &e, int R) { return e.ntok > R ? kCostTwo : kCostOne; }
 __device__ __forceinline__ int item_cost(const Entry &e, int R) { return e.ntok > R ? kCostItemTwo : kCostItemOne; }
